@@ -14,6 +14,8 @@
  *   and the score of a given segmentation with its
  *   gradient, for the training loss                  semicrf_path_score
  *   with boundary projections                        semicrf_*_proj
+ *   other training losses over label scores          semicrf_label_logprob,
+ *   semicrf_policy_loss, semicrf_preference_loss, semicrf_distill_loss
  *
  * Model.  A sequence b has length L_b (0 <= L_b <= T).  A segmentation
  * splits its positions 0..L_b-1 into consecutive segments [s, t) of duration
@@ -101,6 +103,11 @@ enum semicrf_status {
 #define SEMICRF_FLAG_NEGATE_GRAD 0x8u  /* semicrf_path_score subtracts its gradient
                                           (w_b = -grad_score[b]); the other calls
                                           ignore it */
+#define SEMICRF_FLAG_ACCUMULATE 0x10u  /* the label-score losses add their gradient to
+                                          grad_logits (SEMICRF_F32 only) instead of
+                                          writing it */
+#define SEMICRF_FLAG_AVERAGE 0x20u     /* semicrf_preference_loss takes the mean of a
+                                          sequence's log-ratios instead of their sum */
 
 /*
  * Bytes of device workspace needed by forward/backward/viterbi for these
@@ -320,6 +327,146 @@ SEMICRF_API int semicrf_path_score_proj(const float *em, const int32_t *lengths,
                                         float *grad_em, float *grad_trans, float *grad_dur,
                                         float *grad_p_start, float *grad_p_end,
                                         semicrf_stream_t stream);
+
+/*
+ * Training losses over label scores, beside log Z - score(gold): the
+ * log-probabilities of given labels under a softmax per position, a clipped
+ * policy loss with a KL term, a preference loss on pairs of labellings and
+ * distillation from a teacher's top labels.  The scores may be the emissions
+ * [B, T, C] of the model above or an encoder's logits over a vocabulary.
+ * (No counterpart on the pages, which leave the losses in front of the CRF to
+ * the caller.)  Like semicrf_path_score each call computes the loss and, where
+ * grad_logits is not NULL, its gradient, with the upstream weights
+ * grad_loss[b] (device float64; NULL means all ones) given beforehand.
+ *
+ * Common arguments.
+ *  - logits       B * T rows of V scores of type `dtype`, row (b, t) at
+ *                 logits + (b * T + t) * ld elements (ld >= V).
+ *  - grad_logits  rows of the same type, grad_ld apart; every row is written
+ *                 (zeros where a position does not count), or added to under
+ *                 SEMICRF_FLAG_ACCUMULATE.  Must not overlap logits.
+ *  - lengths [B], labels [B, T] int32: position (b, t) counts when
+ *                 t < lengths[b] and labels[b, t] >= 0.  Scores and other
+ *                 per-position inputs of positions that do not count are never
+ *                 read, and they contribute 0 (so does an empty sequence).  A
+ *                 label >= V gives NaN for that position and its sequence's
+ *                 sums, and no gradient row.
+ *  - temperature  z = logits / temperature, 1e-3 <= temperature <= 1e3.
+ *  - ws           semicrf_loss_workspace_bytes(B, T) bytes, 256-byte aligned, not
+ *                 shared by calls that overlap on the GPU.  The status word is
+ *                 written by every call (semicrf_get_status): a length outside
+ *                 [0, T] gives SEMICRF_ERR_BAD_LENGTH, NaN sums and no gradient
+ *                 for that sequence.
+ *  - Output pointers other than the workspace may be NULL where marked.
+ *  - Limits: V <= 2^24, B * T <= 2^27, k <= 1024 (SEMICRF_ERR_UNSUPPORTED).
+ *  - A row holding NaN or +inf, or nothing but -inf, has no softmax: its terms
+ *    and its gradient row are NaN.  -inf beside finite scores is a label of
+ *    probability zero.
+ *  - Sums of exponentials are float32 around the row's maximum; log-probabilities,
+ *    ratios and sums over positions are float64, each output rounded once.
+ *    Results are deterministic (no floating-point atomics).
+ */
+enum semicrf_dtype { SEMICRF_F32 = 0, SEMICRF_BF16 = 1, SEMICRF_F16 = 2 };
+
+SEMICRF_API int semicrf_loss_workspace_bytes(int B, int T, size_t *bytes);
+
+/*
+ * logp[b, t] = z_y - log sum_v exp z_v at the label y = labels[b, t] (0 where
+ * it does not count), score[b] its sum over t (float32, each nullable).
+ *   grad_logits[b, t, v] = grad_logp[b, t] ([v = y] - q_v) / temperature,
+ * q = softmax(z); grad_logp [B, T] float32, NULL means all ones.
+ */
+SEMICRF_API int semicrf_label_logprob(const void *logits, int dtype, int64_t ld,
+                                      const int32_t *lengths, const int32_t *labels, int B, int T,
+                                      int V, double temperature, unsigned flags, void *ws,
+                                      size_t ws_bytes, const float *grad_logp, float *logp,
+                                      float *score, void *grad_logits, int64_t grad_ld,
+                                      semicrf_stream_t stream);
+
+/*
+ * Clipped policy loss.  With r = exp(logp - old_logp), A the advantage
+ * (adv [B], or [B, T] where adv_per_token) and d = ref_logp - logp:
+ *   loss[b] = sum_t -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                   + kl_coef (exp(d) - d - 1)
+ *   grad_logits = grad_loss[b] * d loss[b] / d logits
+ * (on a corner of the clip the unclipped side counts).  old_logp, ref_logp
+ * [B, T] float32; ref_logp NULL: no KL term.  Also kl[b] = sum_t (exp(d) - d -
+ * 1), clipped[b] the number of positions whose gradient the clip removes
+ * (int32), and logp [B, T]; all four outputs are nullable.
+ * 0 <= clip_low <= 1, clip_high >= 0 (may be infinite).
+ */
+SEMICRF_API int semicrf_policy_loss(const void *logits, int dtype, int64_t ld,
+                                    const int32_t *lengths, const int32_t *labels, int B, int T,
+                                    int V, double temperature, const float *old_logp,
+                                    const float *ref_logp, const float *adv, int adv_per_token,
+                                    double clip_low, double clip_high, double kl_coef,
+                                    unsigned flags, void *ws, size_t ws_bytes,
+                                    const double *grad_loss, float *loss, float *kl,
+                                    int32_t *clipped, float *logp, void *grad_logits,
+                                    int64_t grad_ld, semicrf_stream_t stream);
+
+/*
+ * Preference loss on paired log-ratios.  B is even; pair i is the chosen
+ * sequence i and the rejected sequence B/2 + i.  With
+ *   reward[b] = beta * sum_t (logp - ref_logp)   (the mean over the positions
+ *               that count under SEMICRF_FLAG_AVERAGE; ref_logp NULL means 0)
+ *   u_i = reward[i] - reward[B/2 + i] - margin
+ *   loss[i] = -(1 - smoothing) log sigmoid(u_i) - smoothing log sigmoid(-u_i)
+ * grad_logits = grad_loss[i] * d loss[i] / d logits; grad_loss, loss [B/2].
+ * loss, reward and logp [B, T] (float32) are nullable.  A malformed sequence
+ * (a label >= V, a bad length) gives its pair loss NaN and no gradient.
+ */
+SEMICRF_API int semicrf_preference_loss(const void *logits, int dtype, int64_t ld,
+                                        const int32_t *lengths, const int32_t *labels, int B,
+                                        int T, int V, double temperature, const float *ref_logp,
+                                        double beta, double margin, double smoothing,
+                                        unsigned flags, void *ws, size_t ws_bytes,
+                                        const double *grad_loss, float *loss, float *reward,
+                                        float *logp, void *grad_logits, int64_t grad_ld,
+                                        semicrf_stream_t stream);
+
+/*
+ * Distillation from a teacher's top labels.  Position (b, t), t < lengths[b],
+ * has up to k entries: teacher_ids[b, t, j] (int32, negative: unused) with the
+ * teacher's logits teacher_logits[b, t, j] (float32).  With p_j =
+ * softmax(teacher_logits / temperature) over the entries in use, or, where
+ * teacher_lse [B, T] (float32, nullable: the teacher's log sum exp at this
+ * temperature over all labels) is given, exp(teacher_logits / temperature -
+ * teacher_lse):
+ *   token_loss[b, t] = temperature^2 sum_j p_j (log p_j - log q_{id_j})
+ *   loss[b] = sum_t token_loss[b, t],  grad_logits = grad_loss[b] d loss[b] / d logits.
+ * Entries of equal label add up; an entry of logit -inf has p = 0; a position
+ * with no entry of positive probability has loss and gradient 0.  An id >= V
+ * gives NaN and no gradient row.  loss and token_loss are nullable.
+ */
+SEMICRF_API int semicrf_distill_loss(const void *logits, int dtype, int64_t ld,
+                                     const int32_t *lengths, const int32_t *teacher_ids,
+                                     const float *teacher_logits, const float *teacher_lse, int k,
+                                     int B, int T, int V, double temperature, unsigned flags,
+                                     void *ws, size_t ws_bytes, const double *grad_loss,
+                                     float *loss, float *token_loss, void *grad_logits,
+                                     int64_t grad_ld, semicrf_stream_t stream);
+
+/*
+ * The policy and the preference loss on paths: one log-probability (or, for
+ * pairs of labellings of the same input, one path score: log Z cancels) per
+ * segmentation, float64 [N] device arrays, as semicrf_forward and
+ * semicrf_path_score write them.  The gradients are float64 and are what
+ * semicrf_path_score takes as grad_score and semicrf_backward, negated, as
+ * grad_logZ.  Formulas as above with one ratio per path; grad_loss [N] nullable,
+ * outputs nullable.  ref_chosen and ref_rejected are given together or not at all.
+ */
+SEMICRF_API int semicrf_policy_scores(const double *logp, const double *old_logp,
+                                      const double *ref_logp, const double *adv, int N,
+                                      double clip_low, double clip_high, double kl_coef,
+                                      const double *grad_loss, double *loss, double *kl,
+                                      double *grad_logp, semicrf_stream_t stream);
+SEMICRF_API int semicrf_preference_scores(const double *chosen, const double *rejected,
+                                          const double *ref_chosen, const double *ref_rejected,
+                                          int N, double beta, double margin, double smoothing,
+                                          const double *grad_loss, double *loss,
+                                          double *grad_chosen, double *grad_rejected,
+                                          semicrf_stream_t stream);
 
 /*
  * Synchronises `stream`, then reads the device status word of workspace

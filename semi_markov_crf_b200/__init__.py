@@ -14,7 +14,8 @@ _BINDING_NAMES = {
     "workspace_bytes", "prefix_center", "forward", "backward", "viterbi", "get_status",
     "strerror", "SemiCRFError", "library_path", "Workspace", "FLAG_NO_CENTER",
     "FLAG_FORWARD_ONLY", "selftest_bounded_wait", "forward_noalloc", "profile_enable",
-    "profile_read",
+    "profile_read", "LossWorkspace", "loss_workspace_bytes", "label_logprob", "policy_loss",
+    "preference_loss", "distill_loss", "policy_scores", "preference_scores",
 }
 
 

@@ -10,6 +10,7 @@
 
 #include "semicrf.h"
 #include "kernels.cuh"
+#include "loss.cuh"
 
 namespace semicrf {
 
@@ -520,6 +521,30 @@ int run_prefix(const float* em, const int32_t* lengths, const Dims& d, const WsP
 }
 
 }  // namespace
+
+LaunchTimer::LaunchTimer(const char* name, cudaStream_t st) : name_(nullptr), st_(st) {
+  std::lock_guard<std::mutex> g(prof_mu);
+  if (!prof_on) return;
+  if (cudaEventCreate(&a_) != cudaSuccess || cudaEventCreate(&b_) != cudaSuccess) {
+    cudaGetLastError();
+    return;
+  }
+  name_ = name;
+  cudaEventRecord(a_, st_);
+}
+
+LaunchTimer::~LaunchTimer() {
+  if (!name_) return;
+  cudaEventRecord(b_, st_);
+  std::lock_guard<std::mutex> g(prof_mu);
+  try {
+    prof_recs.push_back(ProfRec{name_, a_, b_});
+  } catch (...) {  // out of host memory: the launch goes unrecorded
+    cudaEventDestroy(a_);
+    cudaEventDestroy(b_);
+  }
+}
+
 }  // namespace semicrf
 
 using namespace semicrf;

@@ -1,0 +1,170 @@
+// loss.cuh -- sizes, workspace and launchers of the training losses over rows
+// of label scores (loss_rows.cu, loss_seq.cu, loss_api.cu).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "device.cuh"
+
+namespace semicrf {
+
+constexpr int LOSS_V_MAX = 1 << 24;            // labels per row
+constexpr long long LOSS_ROWS_MAX = 1 << 27;   // B * T
+constexpr int LOSS_K_MAX = 1024;               // teacher entries per position
+
+enum LossMode : int { LM_LOGPROB = 0, LM_POLICY = 1, LM_PREFERENCE = 2, LM_DISTILL = 3 };
+enum LossType : int { LT_F32 = 0, LT_BF16 = 1, LT_F16 = 2 };
+
+// Everything a row kernel reads or writes.  Row r = b * T + t; z = x / temperature.
+struct RowArgs {
+  const void* x;        // [B * T] rows of V scores, ldx elements apart
+  void* g;              // gradient rows (nullptr: none), ldg elements apart
+  long long ldx, ldg;
+  int B, T, V;
+  int add;              // 1: g += gradient (float32 only)
+  const int32_t* lengths;
+  const int32_t* labels;  // [B, T], negative: does not count (not for LM_DISTILL)
+  float sl;             // log2(e) / temperature
+  double s;             // 1 / temperature
+  const float* grad_logp;  // LM_LOGPROB: d loss / d logp [B, T] (nullptr: ones)
+  const float* old_logp;   // LM_POLICY
+  const float* ref_logp;   // LM_POLICY, LM_PREFERENCE; nullptr: no reference
+  const float* adv;        // [B] or, with adv_tok, [B, T]
+  int adv_tok;
+  double clip_lo, clip_hi, kl_coef;  // the clip's corners, the KL term's weight
+  const double* w;         // [B] upstream weights (nullptr: ones)
+  const int32_t* ids;      // LM_DISTILL: [B, T, k] labels, negative: unused entry
+  const float* tl;         // their teacher logits
+  const float* tlse;       // [B, T] teacher log-sum-exp (nullptr: normalise over the entries)
+  int k;
+  float* logp;             // [B, T] output (not LM_DISTILL)
+  float* tok;              // [B, T] per-position term that the sequence pass sums
+  float* kl;               // [B, T] LM_POLICY
+  uint8_t* clip;           // [B, T] LM_POLICY
+  float2* stat;            // [B, T] LM_PREFERENCE: row maximum, sum of exponentials
+  float* wseq;             // [B] LM_PREFERENCE: d loss / d logp of the sequence's positions
+};
+
+// Workspace of the loss entry points: the status word first, as in the
+// recursions' workspace.
+struct LossWs {
+  int* status;
+  float* tok;
+  float* kl;
+  uint8_t* clip;
+  float2* stat;
+  float* wseq;
+};
+size_t loss_layout(int B, int T, void* base, LossWs* p);
+
+// Sums of a sequence's positions and what follows from them (loss_seq.cu).
+struct SeqArgs {
+  int B, T;
+  const int32_t* lengths;
+  const int32_t* labels;   // LM_PREFERENCE: which positions count (for the mean)
+  int* status;
+  const float* tok;
+  const float* kl;
+  const uint8_t* clip;
+  float* sum;              // [B] sums of tok (nullptr: none)
+  float* kl_sum;           // [B] LM_POLICY (nullptr: none)
+  int32_t* clipped;        // [B] LM_POLICY (nullptr: none)
+  // LM_PREFERENCE: sequences [0, B/2) chosen, [B/2, B) rejected
+  double beta, margin, smoothing;
+  int average;
+  const double* w;         // [B/2]
+  float* loss;             // [B/2]
+  float* reward;           // [B] (nullptr: none)
+  float* wseq;             // [B]
+};
+
+cudaError_t launch_loss_rows(int mode, int type, const RowArgs& a, cudaStream_t st);
+// The gradient pass of the preference loss: g = wseq_b / temperature * ([v = y] - q_v).
+cudaError_t launch_loss_scaled(int type, const RowArgs& a, cudaStream_t st);
+cudaError_t launch_loss_sums(const SeqArgs& a, cudaStream_t st);
+cudaError_t launch_loss_pairs(const SeqArgs& a, cudaStream_t st);
+
+cudaError_t launch_policy_scores(const double* logp, const double* old_logp, const double* ref,
+                                 const double* adv, long long n, double clip_lo, double clip_hi,
+                                 double kl_coef, const double* w, double* loss, double* kl,
+                                 double* grad, cudaStream_t st);
+cudaError_t launch_preference_scores(const double* chosen, const double* rejected,
+                                     const double* ref_chosen, const double* ref_rejected,
+                                     long long n, double beta, double margin, double smoothing,
+                                     const double* w, double* loss, double* grad_chosen,
+                                     double* grad_rejected, cudaStream_t st);
+
+// Per-kernel timing of semicrf_profile_enable (api.cu).
+class LaunchTimer {
+ public:
+  LaunchTimer(const char* name, cudaStream_t st);
+  ~LaunchTimer();
+  LaunchTimer(const LaunchTimer&) = delete;
+  LaunchTimer& operator=(const LaunchTimer&) = delete;
+
+ private:
+  const char* name_;
+  cudaStream_t st_;
+  cudaEvent_t a_ = nullptr, b_ = nullptr;
+};
+
+// ---------------------------------------------------------------- shared arithmetic
+// The clipped policy term of one ratio: r = exp(delta), delta = logp - old.
+//   loss = -min(r A, clip(r, 1 - lo, 1 + hi) A) + c (e^d - d - 1),  d = ref - logp
+// and its slope in logp.  On the corners of the clip the unclipped side counts.
+template <typename F>
+struct PolicyTerm {
+  F loss, kl, slope;
+  bool clipped;
+};
+
+__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+
+// e^d - d - 1 without its cancellation: near zero the Taylor series from d^2/2
+// (|d| < 1/2: the first omitted term, d^14/14!, is below 2^-50 of d^2/2).
+template <typename F>
+__device__ __forceinline__ F exp_less_linear(F d) {
+  if (fabs(d) < F(0.5)) {
+    F p = F(1.0 / 6227020800.0);
+    p = p * d + F(1.0 / 479001600.0);
+    p = p * d + F(1.0 / 39916800.0);
+    p = p * d + F(1.0 / 3628800.0);
+    p = p * d + F(1.0 / 362880.0);
+    p = p * d + F(1.0 / 40320.0);
+    p = p * d + F(1.0 / 5040.0);
+    p = p * d + F(1.0 / 720.0);
+    p = p * d + F(1.0 / 120.0);
+    p = p * d + F(1.0 / 24.0);
+    p = p * d + F(1.0 / 6.0);
+    p = p * d + F(0.5);
+    return p * d * d;
+  }
+  return exp_of(d) - d - F(1);
+}
+
+// The clip is given by its corners lo = 1 - clip_low and hi = 1 + clip_high.
+template <typename F>
+__device__ __forceinline__ PolicyTerm<F> policy_term(F delta, F adv, F lo, F hi, F c, bool has_ref,
+                                                     F d) {
+  PolicyTerm<F> o;
+  const F r = exp_of(delta);
+  const F rc = r < lo ? lo : (r > hi ? hi : r);  // NaN stays NaN
+  const F free_ = r * adv, cut = rc * adv;
+  o.clipped = (adv > F(0) && r > hi) || (adv < F(0) && r < lo);
+  o.loss = -(cut < free_ ? cut : free_);
+  o.slope = o.clipped ? F(0) : -free_;
+  o.kl = F(0);
+  if (has_ref) {
+    o.kl = exp_less_linear(d);
+    if (c != F(0)) {
+      o.loss += c * o.kl;
+      o.slope -= c * (fabs(d) < F(0.5) ? d + o.kl : exp_of(d) - F(1));
+    }
+  }
+  return o;
+}
+
+}  // namespace semicrf

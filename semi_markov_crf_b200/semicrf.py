@@ -18,6 +18,9 @@ __all__ = ["workspace_bytes", "workspace_itemize", "WS_GROUPS", "launch_shape", 
            "strerror", "SemiCRFError", "library_path", "Workspace", "FLAG_NO_CENTER",
            "FLAG_FORWARD_ONLY", "FLAG_LOG_DOMAIN", "selftest_bounded_wait", "selftest_bounds", "ring_domains", "profile_enable", "profile_read",
            "forward_noalloc", "NOALLOC_SCRATCH_BYTES",
+           "FLAG_ACCUMULATE", "FLAG_AVERAGE", "LossWorkspace", "loss_workspace_bytes",
+           "label_logprob", "policy_loss", "preference_loss", "distill_loss", "policy_scores",
+           "preference_scores",
            "KERNELS", "lib"]
 
 # every kernel the library launches (names used by the profiler)
@@ -26,12 +29,15 @@ KERNELS = ("prefix_reduce_kernel", "prefix_scan_kernel", "chain_exp_kernel", "ch
            "finalize_positions_kernel",
            "reduce_partials_kernel", "viterbi_kernel", "viterbi_pipe_kernel", "viterbi_argmax_kernel",
            "viterbi_words_kernel", "viterbi_walk_kernel", "path_terms_kernel", "path_grad_kernel",
-           "proj_grad_kernel")
+           "proj_grad_kernel", "loss_rows_kernel", "loss_sums_kernel", "loss_pairs_kernel",
+           "loss_scaled_kernel", "policy_scores_kernel", "preference_scores_kernel")
 
 FLAG_NO_CENTER = 0x1
 FLAG_FORWARD_ONLY = 0x2
 FLAG_LOG_DOMAIN = 0x4
 FLAG_NEGATE_GRAD = 0x8
+FLAG_ACCUMULATE = 0x10
+FLAG_AVERAGE = 0x20
 NOALLOC_SCRATCH_BYTES = 32 << 20  # SEMICRF_NOALLOC_SCRATCH_BYTES
 
 # SEMICRF_LIBRARY=check loads the bounds-checking debug build instead
@@ -47,6 +53,8 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _u = ctypes.c_uint
 _sz = ctypes.c_size_t
+_ll = ctypes.c_int64
+_d = ctypes.c_double
 
 lib.semicrf_workspace_bytes.argtypes = [_i, _i, _i, _i, _u, ctypes.POINTER(_sz)]
 lib.semicrf_workspace_itemize.argtypes = [_i, _i, _i, _i, _u, ctypes.POINTER(_sz), _i]
@@ -69,6 +77,18 @@ lib.semicrf_viterbi_proj.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _
                                      _vp, _vp, _vp, _vp]
 lib.semicrf_path_score_proj.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _u,
                                         _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+lib.semicrf_loss_workspace_bytes.argtypes = [_i, _i, ctypes.POINTER(_sz)]
+lib.semicrf_label_logprob.argtypes = [_vp, _i, _ll, _vp, _vp, _i, _i, _i, _d, _u, _vp, _sz, _vp,
+                                      _vp, _vp, _vp, _ll, _vp]
+lib.semicrf_policy_loss.argtypes = [_vp, _i, _ll, _vp, _vp, _i, _i, _i, _d, _vp, _vp, _vp, _i, _d,
+                                    _d, _d, _u, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _ll, _vp]
+lib.semicrf_preference_loss.argtypes = [_vp, _i, _ll, _vp, _vp, _i, _i, _i, _d, _vp, _d, _d, _d,
+                                        _u, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _ll, _vp]
+lib.semicrf_distill_loss.argtypes = [_vp, _i, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _d, _u, _vp,
+                                     _sz, _vp, _vp, _vp, _vp, _ll, _vp]
+lib.semicrf_policy_scores.argtypes = [_vp, _vp, _vp, _vp, _i, _d, _d, _d, _vp, _vp, _vp, _vp, _vp]
+lib.semicrf_preference_scores.argtypes = [_vp, _vp, _vp, _vp, _i, _d, _d, _d, _vp, _vp, _vp, _vp,
+                                          _vp]
 lib.semicrf_get_status.argtypes = [_vp, _vp, ctypes.POINTER(_i)]
 lib.semicrf_strerror.argtypes = [_i]
 lib.semicrf_strerror.restype = ctypes.c_char_p
@@ -83,7 +103,9 @@ lib.semicrf_profile_read.argtypes = [ctypes.c_char_p, ctypes.POINTER(ctypes.c_do
 for _f in ("semicrf_backward_segments", "semicrf_launch_shape", "semicrf_workspace_itemize", "semicrf_forward_noalloc", "semicrf_profile_enable", "semicrf_profile_read", "semicrf_workspace_bytes", "semicrf_prefix_center", "semicrf_forward",
            "semicrf_backward", "semicrf_viterbi", "semicrf_path_score", "semicrf_get_status",
            "semicrf_forward_proj", "semicrf_backward_proj", "semicrf_viterbi_proj",
-           "semicrf_path_score_proj",
+           "semicrf_path_score_proj", "semicrf_loss_workspace_bytes", "semicrf_label_logprob",
+           "semicrf_policy_loss", "semicrf_preference_loss", "semicrf_distill_loss",
+           "semicrf_policy_scores", "semicrf_preference_scores",
            "semicrf_selftest_bounded_wait", "semicrf_selftest_bounds", "semicrf_ring_domains"):
     getattr(lib, _f).restype = _i
 
@@ -397,7 +419,290 @@ def path_score(em, lengths, trans, dur, labels, seg_start, center: bool = True,
     return score
 
 
-def get_status(ws: Workspace) -> int:
+# ------------------------------------------------ training losses over label scores
+_LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def loss_workspace_bytes(B: int, T: int) -> int:
+    n = _sz(0)
+    _check(lib.semicrf_loss_workspace_bytes(B, T, ctypes.byref(n)), "semicrf_loss_workspace_bytes")
+    return int(n.value)
+
+
+class LossWorkspace:
+    """Device workspace of the label-score losses for (B, T).  Calls that may
+    overlap on the GPU (two streams, two captured graphs) need one each."""
+
+    def __init__(self, B: int, T: int, device=None):
+        self.dims = (B, T)
+        self.nbytes = loss_workspace_bytes(B, T)
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+
+    @property
+    def ptr(self) -> int:
+        return self.buf.data_ptr()
+
+
+def _row_stride(t, name) -> int:
+    """Elements between the rows of a [B, T, V] tensor whose rows are contiguous
+    and evenly spaced (a slice of a padded last dimension is)."""
+    B, T, V = t.shape
+    sb, st, sv = t.stride()
+    if B * T == 0:
+        return V
+    if sv != 1 and V > 1:
+        raise TypeError(f"the last dimension of {name} must be contiguous")
+    ld = st if T > 1 else (sb if B > 1 else V)
+    if ld < V or (B > 1 and sb != T * ld):
+        raise TypeError(f"{name} must have evenly spaced rows that do not overlap")
+    return ld
+
+
+def _logit_rows(logits, lengths, name="logits"):
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 3 \
+            or logits.dtype not in _LOGIT_TYPES:
+        raise TypeError(f"{name} must be a CUDA float32, bfloat16 or float16 tensor [B, T, V]")
+    B, T, V = logits.shape
+    _shaped(lengths, torch.int32, "lengths", logits.device, (B,))
+    return B, T, V, _row_stride(logits, name)
+
+
+def _shaped(t, dtype, name, device, shape):
+    _need(t, dtype, name, device)
+    if t.shape != shape:
+        raise TypeError(f"{name} must have shape {tuple(shape)}")
+    return t
+
+
+def _loss_out(out, name, shape, dtype, device):
+    """out[name], made where it is missing and checked where it is not."""
+    t = out.get(name)
+    if t is None:
+        t = out[name] = torch.empty(shape, dtype=dtype, device=device)
+        return t
+    return _shaped(t, dtype, name, device, shape)
+
+
+def _loss_grad(out, logits, grad, accumulate):
+    """(pointer, row stride) of out["grad_logits"]; (None, 0) without a gradient."""
+    if not grad:
+        return None, 0
+    g = out.get("grad_logits")
+    if g is None:
+        if accumulate:
+            raise ValueError("accumulate needs out['grad_logits'] to add to")
+        g = out["grad_logits"] = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        return g.data_ptr(), logits.shape[2]
+    if g.dtype != logits.dtype or g.shape != logits.shape or g.device != logits.device:
+        raise TypeError("grad_logits must have the type, shape and device of logits")
+    return g.data_ptr(), _row_stride(g, "grad_logits")
+
+
+def _loss_ws(ws, B, T, device):
+    if ws is None or ws.dims != (B, T):
+        return LossWorkspace(B, T, device)
+    if ws.buf.device != device:
+        raise TypeError(f"ws is on {ws.buf.device}, expected {device}")
+    return ws
+
+
+def _launch(fn, where, device, *args):
+    """Calls fn(*args, stream) with `device` current."""
+    index = device.index
+    if index is None or index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc:
+        _check(rc, where)
+
+
+def label_logprob(logits, lengths, labels, temperature: float = 1.0, grad_logp=None,
+                  grad: bool = False, accumulate: bool = False, ws: LossWorkspace | None = None,
+                  out: dict | None = None):
+    """Log-probabilities of given labels under a softmax per position
+    (semicrf_label_logprob): a dict with ``logp`` [B,T] and ``score`` [B]
+    (float32) and, with ``grad``, ``grad_logits`` = grad_logp * d logp / d
+    logits (``grad_logp`` [B,T] float32, None = ones).
+
+    ``logits`` [B,T,V] float32, bfloat16 or float16 (a slice of a padded last
+    dimension will do), ``lengths`` [B] int32, ``labels`` [B,T] int32, negative
+    where the position does not count.  Here and in the other losses ``out``
+    may supply preallocated outputs, ``accumulate`` adds the gradient to
+    out["grad_logits"] (float32), and ``ws`` is a :class:`LossWorkspace`, whose
+    status :func:`get_status` reads."""
+    B, T, V, ld = _logit_rows(logits, lengths)
+    dev = logits.device
+    _shaped(labels, torch.int32, "labels", dev, (B, T))
+    if grad_logp is not None:
+        _shaped(grad_logp, torch.float32, "grad_logp", dev, (B, T))
+    o = {} if out is None else out
+    ws = _loss_ws(ws, B, T, dev)
+    logp = _loss_out(o, "logp", (B, T), torch.float32, dev)
+    score = _loss_out(o, "score", (B,), torch.float32, dev)
+    g, ldg = _loss_grad(o, logits, grad, accumulate)
+    _launch(lib.semicrf_label_logprob, "semicrf_label_logprob", dev, logits.data_ptr(),
+            _LOGIT_TYPES[logits.dtype], ld, lengths.data_ptr(), labels.data_ptr(), B, T, V,
+            temperature, FLAG_ACCUMULATE if accumulate else 0, ws.ptr, ws.nbytes, _ptr(grad_logp),
+            logp.data_ptr(), score.data_ptr(), g, ldg)
+    return o
+
+
+def policy_loss(logits, lengths, labels, old_logp, adv, ref_logp=None, clip_low: float = 0.2,
+                clip_high: float = 0.2, kl_coef: float = 0.0, temperature: float = 1.0,
+                grad_loss=None, grad: bool = True, accumulate: bool = False,
+                ws: LossWorkspace | None = None, out: dict | None = None):
+    """Clipped policy loss with a KL term (semicrf_policy_loss): a dict with
+    ``loss`` and ``kl`` [B] and ``logp`` [B,T] (float32), ``clipped`` [B] int32
+    and, with ``grad``, ``grad_logits`` = grad_loss * d loss / d logits.
+
+    ``old_logp`` and ``ref_logp`` [B,T] float32 are the log-probabilities of the
+    labels under the policy that drew them and under the reference (None: no
+    KL term), ``adv`` [B] or [B,T] float32 the advantages, ``grad_loss`` [B]
+    float64 the upstream weights (None = ones).  The rest as for
+    :func:`label_logprob`."""
+    B, T, V, ld = _logit_rows(logits, lengths)
+    dev = logits.device
+    _shaped(labels, torch.int32, "labels", dev, (B, T))
+    _shaped(old_logp, torch.float32, "old_logp", dev, (B, T))
+    per_token = isinstance(adv, torch.Tensor) and adv.dim() == 2
+    _shaped(adv, torch.float32, "adv", dev, (B, T) if per_token else (B,))
+    if ref_logp is not None:
+        _shaped(ref_logp, torch.float32, "ref_logp", dev, (B, T))
+    if grad_loss is not None:
+        _shaped(grad_loss, torch.float64, "grad_loss", dev, (B,))
+    o = {} if out is None else out
+    ws = _loss_ws(ws, B, T, dev)
+    loss = _loss_out(o, "loss", (B,), torch.float32, dev)
+    kl = _loss_out(o, "kl", (B,), torch.float32, dev)
+    clipped = _loss_out(o, "clipped", (B,), torch.int32, dev)
+    logp = _loss_out(o, "logp", (B, T), torch.float32, dev)
+    g, ldg = _loss_grad(o, logits, grad, accumulate)
+    _launch(lib.semicrf_policy_loss, "semicrf_policy_loss", dev, logits.data_ptr(),
+            _LOGIT_TYPES[logits.dtype], ld, lengths.data_ptr(), labels.data_ptr(), B, T, V,
+            temperature, old_logp.data_ptr(), _ptr(ref_logp), adv.data_ptr(), per_token, clip_low,
+            clip_high, kl_coef, FLAG_ACCUMULATE if accumulate else 0, ws.ptr, ws.nbytes,
+            _ptr(grad_loss), loss.data_ptr(), kl.data_ptr(), clipped.data_ptr(), logp.data_ptr(), g,
+            ldg)
+    return o
+
+
+def preference_loss(logits, lengths, labels, ref_logp=None, beta: float = 0.1, margin: float = 0.0,
+                    smoothing: float = 0.0, average: bool = False, temperature: float = 1.0,
+                    grad_loss=None, grad: bool = True, accumulate: bool = False,
+                    ws: LossWorkspace | None = None, out: dict | None = None):
+    """Preference loss on paired log-ratios (semicrf_preference_loss).  The
+    first half of the batch holds the chosen sequences, the second half the
+    rejected ones, in the same order.  A dict with ``loss`` [B/2], ``reward``
+    [B] and ``logp`` [B,T] (float32) and, with ``grad``, ``grad_logits``.
+    ``ref_logp`` [B,T] float32 (None = 0), ``grad_loss`` [B/2] float64;
+    ``average`` takes the mean log-ratio of a sequence.  The rest as for
+    :func:`label_logprob`."""
+    B, T, V, ld = _logit_rows(logits, lengths)
+    dev = logits.device
+    _shaped(labels, torch.int32, "labels", dev, (B, T))
+    if ref_logp is not None:
+        _shaped(ref_logp, torch.float32, "ref_logp", dev, (B, T))
+    if grad_loss is not None:
+        _shaped(grad_loss, torch.float64, "grad_loss", dev, (B // 2,))
+    o = {} if out is None else out
+    ws = _loss_ws(ws, B, T, dev)
+    loss = _loss_out(o, "loss", (B // 2,), torch.float32, dev)
+    reward = _loss_out(o, "reward", (B,), torch.float32, dev)
+    logp = _loss_out(o, "logp", (B, T), torch.float32, dev)
+    g, ldg = _loss_grad(o, logits, grad, accumulate)
+    _launch(lib.semicrf_preference_loss, "semicrf_preference_loss", dev, logits.data_ptr(),
+            _LOGIT_TYPES[logits.dtype], ld, lengths.data_ptr(), labels.data_ptr(), B, T, V,
+            temperature, _ptr(ref_logp), beta, margin, smoothing,
+            (FLAG_ACCUMULATE if accumulate else 0) | (FLAG_AVERAGE if average else 0), ws.ptr,
+            ws.nbytes, _ptr(grad_loss), loss.data_ptr(), reward.data_ptr(), logp.data_ptr(), g, ldg)
+    return o
+
+
+def distill_loss(logits, lengths, teacher_ids, teacher_logits, teacher_lse=None,
+                 temperature: float = 1.0, grad_loss=None, grad: bool = True,
+                 accumulate: bool = False, ws: LossWorkspace | None = None,
+                 out: dict | None = None):
+    """Distillation from a teacher's top labels (semicrf_distill_loss): a dict
+    with ``loss`` [B] and ``token_loss`` [B,T] (float32) and, with ``grad``,
+    ``grad_logits``.  ``teacher_ids`` [B,T,k] int32 (negative: unused entry),
+    ``teacher_logits`` [B,T,k] float32; ``teacher_lse`` [B,T] float32 is the
+    teacher's log-sum-exp over all labels at this temperature (None: its
+    probabilities are normalised over the entries).  ``grad_loss`` [B]
+    float64.  The rest as for :func:`label_logprob`."""
+    B, T, V, ld = _logit_rows(logits, lengths)
+    dev = logits.device
+    if not isinstance(teacher_ids, torch.Tensor) or teacher_ids.dim() != 3:
+        raise TypeError("teacher_ids must be a tensor [B, T, k]")
+    k = teacher_ids.shape[2]
+    _shaped(teacher_ids, torch.int32, "teacher_ids", dev, (B, T, k))
+    _shaped(teacher_logits, torch.float32, "teacher_logits", dev, (B, T, k))
+    if teacher_lse is not None:
+        _shaped(teacher_lse, torch.float32, "teacher_lse", dev, (B, T))
+    if grad_loss is not None:
+        _shaped(grad_loss, torch.float64, "grad_loss", dev, (B,))
+    o = {} if out is None else out
+    ws = _loss_ws(ws, B, T, dev)
+    loss = _loss_out(o, "loss", (B,), torch.float32, dev)
+    token = _loss_out(o, "token_loss", (B, T), torch.float32, dev)
+    g, ldg = _loss_grad(o, logits, grad, accumulate)
+    _launch(lib.semicrf_distill_loss, "semicrf_distill_loss", dev, logits.data_ptr(),
+            _LOGIT_TYPES[logits.dtype], ld, lengths.data_ptr(), teacher_ids.data_ptr(),
+            teacher_logits.data_ptr(), _ptr(teacher_lse), k, B, T, V, temperature,
+            FLAG_ACCUMULATE if accumulate else 0, ws.ptr, ws.nbytes, _ptr(grad_loss),
+            loss.data_ptr(), token.data_ptr(), g, ldg)
+    return o
+
+
+def policy_scores(logp, old_logp, adv, ref_logp=None, clip_low: float = 0.2,
+                  clip_high: float = 0.2, kl_coef: float = 0.0, grad_loss=None,
+                  out: dict | None = None):
+    """The policy loss on paths (semicrf_policy_scores): one ratio per sampled
+    segmentation, from logp = :func:`path_score` - log Z.  All float64 [N].
+    Returns a dict with ``loss``, ``kl`` and ``grad_logp`` = grad_loss * d loss
+    / d logp, which is the grad_score of :func:`path_score` and, negated, the
+    grad_logZ of :func:`backward`."""
+    if not isinstance(logp, torch.Tensor) or logp.dim() != 1:
+        raise TypeError("logp must be a tensor [N]")
+    dev, n = logp.device, logp.shape
+    for name, t in (("logp", logp), ("old_logp", old_logp), ("adv", adv), ("ref_logp", ref_logp),
+                    ("grad_loss", grad_loss)):
+        if t is not None or name in ("old_logp", "adv"):
+            _shaped(t, torch.float64, name, dev, n)
+    o = {} if out is None else out
+    loss, kl, g = (_loss_out(o, name, n, torch.float64, dev) for name in ("loss", "kl", "grad_logp"))
+    _launch(lib.semicrf_policy_scores, "semicrf_policy_scores", dev, logp.data_ptr(),
+            old_logp.data_ptr(), _ptr(ref_logp), adv.data_ptr(), n[0], clip_low, clip_high, kl_coef,
+            _ptr(grad_loss), loss.data_ptr(), kl.data_ptr(), g.data_ptr())
+    return o
+
+
+def preference_scores(chosen, rejected, ref_chosen=None, ref_rejected=None, beta: float = 0.1,
+                      margin: float = 0.0, smoothing: float = 0.0, grad_loss=None,
+                      out: dict | None = None):
+    """The preference loss on path scores (semicrf_preference_scores): pairs of
+    segmentations of the same inputs, so that log Z cancels.  All float64 [N];
+    the reference's scores are given together or not at all.  Returns a dict
+    with ``loss``, ``grad_chosen`` and ``grad_rejected``, the grad_score of the
+    two :func:`path_score` calls."""
+    if not isinstance(chosen, torch.Tensor) or chosen.dim() != 1:
+        raise TypeError("chosen must be a tensor [N]")
+    dev, n = chosen.device, chosen.shape
+    for name, t in (("chosen", chosen), ("rejected", rejected), ("ref_chosen", ref_chosen),
+                    ("ref_rejected", ref_rejected), ("grad_loss", grad_loss)):
+        if t is not None or name == "rejected":
+            _shaped(t, torch.float64, name, dev, n)
+    o = {} if out is None else out
+    loss, gc, gr = (_loss_out(o, name, n, torch.float64, dev)
+                    for name in ("loss", "grad_chosen", "grad_rejected"))
+    _launch(lib.semicrf_preference_scores, "semicrf_preference_scores", dev, chosen.data_ptr(),
+            rejected.data_ptr(), _ptr(ref_chosen), _ptr(ref_rejected), n[0], beta, margin,
+            smoothing, _ptr(grad_loss), loss.data_ptr(), gc.data_ptr(), gr.data_ptr())
+    return o
+
+
+def get_status(ws: Workspace | LossWorkspace) -> int:
     """Synchronises the current stream and returns the workspace status word."""
     st = _i(0)
     _check(lib.semicrf_get_status(ws.ptr, _stream(ws.buf.device), ctypes.byref(st)),
