@@ -1,5 +1,5 @@
 // loss.cuh -- sizes, workspace and launchers of the training losses over rows
-// of label scores (loss_rows.cu, loss_seq.cu, loss_api.cu).
+// of label scores (loss_row.cuh, loss_seq.cu, loss_api.cu).
 #pragma once
 
 #include <cstddef>
@@ -14,7 +14,9 @@ constexpr int LOSS_V_MAX = 1 << 24;            // labels per row
 constexpr long long LOSS_ROWS_MAX = 1 << 27;   // B * T
 constexpr int LOSS_K_MAX = 1024;               // teacher entries per position
 
-enum LossMode : int { LM_LOGPROB = 0, LM_POLICY = 1, LM_PREFERENCE = 2, LM_DISTILL = 3 };
+// LM_SCALED: the gradient pass of the preference loss, g = wseq_b / temperature ([v = y] - q_v)
+// from the statistics that its first pass left.
+enum LossMode : int { LM_LOGPROB = 0, LM_POLICY = 1, LM_PREFERENCE = 2, LM_DISTILL = 3, LM_SCALED = 4 };
 enum LossType : int { LT_F32 = 0, LT_BF16 = 1, LT_F16 = 2 };
 
 // Everything a row kernel reads or writes.  Row r = b * T + t; z = x / temperature.
@@ -43,8 +45,9 @@ struct RowArgs {
   float* tok;              // [B, T] per-position term that the sequence pass sums
   float* kl;               // [B, T] LM_POLICY
   uint8_t* clip;           // [B, T] LM_POLICY
-  float2* stat;            // [B, T] LM_PREFERENCE: row maximum, sum of exponentials
-  float* wseq;             // [B] LM_PREFERENCE: d loss / d logp of the sequence's positions
+  float2* stat;            // [B, T] LM_PREFERENCE: a row's base and sum of exponentials
+  float* wseq;             // [B] LM_SCALED: d loss / d logp of the sequence's positions
+  int* status;             // cleared by the pass (nullptr: left alone)
 };
 
 // Workspace of the loss entry points: the status word first, as in the
@@ -80,9 +83,16 @@ struct SeqArgs {
   float* wseq;             // [B]
 };
 
-cudaError_t launch_loss_rows(int mode, int type, const RowArgs& a, cudaStream_t st);
-// The gradient pass of the preference loss: g = wseq_b / temperature * ([v = y] - q_v).
-cudaError_t launch_loss_scaled(int type, const RowArgs& a, cudaStream_t st);
+// One pass over the rows (loss_row.cuh, compiled once for each type).
+cudaError_t launch_rows_f32(int mode, const RowArgs& a, cudaStream_t st);
+cudaError_t launch_rows_bf16(int mode, const RowArgs& a, cudaStream_t st);
+cudaError_t launch_rows_f16(int mode, const RowArgs& a, cudaStream_t st);
+
+inline cudaError_t launch_loss_rows(int mode, int type, const RowArgs& a, cudaStream_t st) {
+  return type == LT_F32 ? launch_rows_f32(mode, a, st)
+                        : type == LT_BF16 ? launch_rows_bf16(mode, a, st) : launch_rows_f16(mode, a, st);
+}
+int loss_sm_count();  // of the current device
 cudaError_t launch_loss_sums(const SeqArgs& a, cudaStream_t st);
 cudaError_t launch_loss_pairs(const SeqArgs& a, cudaStream_t st);
 

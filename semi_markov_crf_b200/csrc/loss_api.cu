@@ -83,11 +83,15 @@ int prepare_rows(const void* logits, int dtype, int64_t ld, const int32_t* lengt
   a.lengths = lengths;
   a.s = 1.0 / temperature;
   a.sl = (float)(LOG2E_D / temperature);
+  a.status = p.status;
   return SEMICRF_OK;
 }
 
 int run_rows(int mode, int dtype, const RowArgs& a, cudaStream_t st) {
-  if (a.T == 0) return SEMICRF_OK;
+  if (a.T == 0)  // no rows: the pass that clears the status word does not run
+    return !a.status || cudaMemsetAsync(a.status, 0, sizeof(int), st) == cudaSuccess
+               ? SEMICRF_OK
+               : SEMICRF_ERR_CUDA;
   LaunchTimer lt("loss_rows_kernel", st);
   return launch_loss_rows(mode, dtype, a, st) == cudaSuccess ? SEMICRF_OK : SEMICRF_ERR_CUDA;
 }
@@ -120,6 +124,17 @@ bool clip_ok(double lo, double hi, double kl) {
 }
 
 }  // namespace
+
+int loss_sm_count() {
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v < 1) {
+    cudaGetLastError();
+    return 148;  // B200
+  }
+  return v;
+}
+
 }  // namespace semicrf
 
 using namespace semicrf;
@@ -236,9 +251,9 @@ extern "C" int semicrf_preference_loss(const void* logits, int dtype, int64_t ld
     LaunchTimer lt("loss_pairs_kernel", st);
     if (launch_loss_pairs(q, st) != cudaSuccess) return SEMICRF_ERR_CUDA;
   }
-  if (!grad_logits || T == 0) return SEMICRF_OK;
-  LaunchTimer lt("loss_scaled_kernel", st);
-  return launch_loss_scaled(dtype, a, st) == cudaSuccess ? SEMICRF_OK : SEMICRF_ERR_CUDA;
+  if (!grad_logits) return SEMICRF_OK;
+  a.status = nullptr;
+  return run_rows(LM_SCALED, dtype, a, st);
 }
 
 extern "C" int semicrf_distill_loss(const void* logits, int dtype, int64_t ld,

@@ -1,0 +1,424 @@
+// loss_row.cuh -- one pass over rows of label scores: the log-sum-exp of a
+// row, the loss term of its position and the gradient row.
+//
+// With z = x / temperature, q = softmax(z) and lse = log sum exp z:
+//   label losses   logp = z_y - lse;  d logp / d x_v = ([v = y] - q_v) / temperature
+//                  so a position with d loss / d logp = a gets the row
+//                  a / temperature * ([v = y] - q_v)
+//   distillation   p_j over the teacher's entries j (labels id_j):
+//                  loss = temperature^2 * sum_j p_j (log p_j - log q_{id_j});
+//                  row  = temperature * (P q_v - sum_{j: id_j = v} p_j),  P = sum_j p_j
+//
+// A position costs one read of its V scores, and one write of V gradient
+// entries: bytes bound it (about five float32 operations and one exponential
+// an element).  Sums of exponentials are float32 relative to the running
+// maximum, which is kept in the scores' own units so that rows masked with
+// the type's lowest value still have a softmax; what follows from them for a
+// position (logp, the ratio, the loss) is float64 or exact differences.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "loss.cuh"
+
+namespace semicrf {
+
+namespace {
+
+// ------------------------------------------------------------------ elements
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+__device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
+
+// ------------------------------------------------------- exponentials of a row
+// Exponentials are taken in base 2 around the row's scaled maximum mb = m sl
+// (sl = log2(e) / temperature): 2^(x sl - mb), one fused multiply-add and one
+// ex2 an element.  Where m sl leaves float32's range (a row whose scores all
+// sit at the type's lowest value) they are 2^((x - m) sl) instead.
+struct Base {
+  float at;     // mb, or m where not direct
+  bool direct;
+};
+
+constexpr float F32_MAX = 3.402823466e38f;
+
+__device__ __forceinline__ Base make_base(float m, float sl) {
+  const float mb = m * sl;
+  Base h;
+  h.direct = fabsf(mb) <= F32_MAX;
+  h.at = h.direct ? mb : m;
+  return h;
+}
+
+__device__ __forceinline__ float based_exp(float x, float sl, const Base& h) {
+  return ex2(h.direct ? fmaf(x, sl, -h.at) : (x - h.at) * sl);
+}
+
+// The base in the scores' units.  sl is rounded to float32; taking the base
+// over that same factor keeps its error out of the dominant terms of the sum.
+__device__ __forceinline__ double base_score(const Base& h, float sl) {
+  return h.direct ? (double)h.at / (double)sl : (double)h.at;
+}
+
+// (base, sum) of a row in one float2: a sum is positive, so its sign tells which base it is.
+__device__ __forceinline__ float2 pack_stat(const Base& h, float S) {
+  return make_float2(h.at, h.direct ? S : -S);
+}
+__device__ __forceinline__ Base unpack_stat(float2 v, float& S) {
+  Base h;
+  h.at = v.x;
+  h.direct = !signbit(v.y);
+  S = h.direct ? v.y : -v.y;
+  return h;
+}
+
+// log S for S = 1 .. V: exponent and mantissa apart, so that the error is that
+// of log2 on [1, 2) whatever V is.
+__device__ __forceinline__ double log_of_sum(float S) {
+  if (!(S > 0.0f && S <= F32_MAX)) return (double)logf(S);
+  const int bits = __float_as_int(S);
+  const float mant = __int_as_float((bits & 0x007fffff) | 0x3f800000);
+  return LN2_D * ((double)((bits >> 23) - 127) + (double)log2f(mant));
+}
+
+// ------------------------------------------------------------ rows in memory
+template <typename T>
+__device__ __forceinline__ T* row_at(const void* base, long long r, long long ld) {
+  return static_cast<T*>(const_cast<void*>(base)) + r * ld;
+}
+
+// A row's head: whether its position counts, its label.
+struct Head {
+  int b;
+  bool live;       // counts: the row is read and the loss term computed
+  bool malformed;  // counts, but the label lies outside [0, V)
+  int y;
+};
+
+// The two loads behind a head, so that they can be issued a row ahead.
+struct HeadLoad {
+  int b, t, L, y;
+};
+
+constexpr bool has_label(int mode) { return mode != LM_DISTILL; }
+
+template <int MODE>
+__device__ __forceinline__ HeadLoad load_head(const RowArgs& a, long long r) {
+  HeadLoad l;
+  l.b = (int)((unsigned)r / (unsigned)a.T);  // r < 2^27
+  l.t = (int)r - l.b * a.T;
+  l.L = a.lengths[l.b];
+  l.y = has_label(MODE) ? a.labels[r] : 0;
+  return l;
+}
+
+template <int MODE>
+__device__ __forceinline__ Head make_head(const RowArgs& a, const HeadLoad& l) {
+  Head h;
+  h.b = l.b;
+  h.live = l.L <= a.T && l.t < l.L && l.y >= 0;
+  h.y = l.y;
+  h.malformed = has_label(MODE) && h.live && l.y >= a.V;
+  return h;
+}
+
+// The per-position inputs of a label loss, loaded when its row starts.
+struct LabelIn {
+  float xy;  // score of the label
+  float slope, old_logp, ref_logp, adv;
+  double w;
+};
+
+template <typename T, int MODE>
+__device__ __forceinline__ LabelIn load_label(const RowArgs& a, long long r, const Head& h,
+                                              const T* x) {
+  LabelIn in{};
+  in.w = 1.0;
+  if (!has_label(MODE)) return in;
+  in.xy = to_f32<T>(x[h.y]);
+  if (MODE == LM_LOGPROB) in.slope = a.grad_logp ? a.grad_logp[r] : 1.0f;
+  if (MODE == LM_PREFERENCE || MODE == LM_POLICY) in.ref_logp = a.ref_logp ? a.ref_logp[r] : 0.0f;
+  if (MODE == LM_POLICY) {
+    in.old_logp = a.old_logp[r];
+    in.adv = a.adv[a.adv_tok ? r : (long long)h.b];
+  }
+  if (a.w) in.w = a.w[h.b];
+  return in;
+}
+
+// The outputs of a position that does not count, or whose labels are malformed.
+template <int MODE>
+__device__ __forceinline__ void blank_outputs(const RowArgs& a, long long r, bool malformed) {
+  const float v = malformed ? quiet_nan() : 0.0f;
+  if (a.tok) a.tok[r] = v;
+  if (has_label(MODE) && a.logp) a.logp[r] = v;
+  if (MODE == LM_POLICY) {
+    if (a.kl) a.kl[r] = v;
+    if (a.clip) a.clip[r] = 0;
+  }
+}
+
+// What follows from a row's base and sum for a label loss: the position's
+// outputs (written by one thread) and d loss / d logp / temperature.
+template <int MODE>
+__device__ __forceinline__ float label_outputs(const RowArgs& a, long long r, const LabelIn& in,
+                                               const Base& h, float S, bool writer) {
+  const double logp = ((double)in.xy - base_score(h, a.sl)) * a.s - log_of_sum(S);
+  float slope = in.slope;
+  float term = (float)logp;
+  if (MODE == LM_PREFERENCE) term = (float)(logp - (double)in.ref_logp);
+  if (MODE == LM_POLICY) {
+    const PolicyTerm<float> o =
+        policy_term<float>((float)(logp - (double)in.old_logp), in.adv, (float)a.clip_lo,
+                           (float)a.clip_hi, (float)a.kl_coef, a.ref_logp != nullptr,
+                           (float)((double)in.ref_logp - logp));
+    term = o.loss;
+    slope = o.slope;
+    if (writer) {
+      if (a.kl) a.kl[r] = o.kl;
+      if (a.clip) a.clip[r] = o.clipped;
+    }
+  }
+  if (writer) {
+    if (a.tok) a.tok[r] = term;
+    if (a.logp) a.logp[r] = (float)logp;
+    if (MODE == LM_PREFERENCE) a.stat[r] = pack_stat(h, S);
+  }
+  return (float)(in.w * (double)slope * a.s);
+}
+
+// ------------------------------------------------------ the teacher's entries
+// Kept in shared memory by the lanes that look after them.
+struct Teacher {
+  float* p;    // [k] logits, then probabilities
+  int* id;     // [k]
+  float* x;    // [k] the row's scores at those labels
+  float* old;  // [k] the gradient's value before this call (accumulation)
+};
+
+constexpr int TEACHER_WORDS = 4;
+
+struct TeacherHead {
+  float tm, tlog, P;
+  bool malformed;
+};
+
+// The elements of a row that a CTA writes: [lo, hi) and those from `tail` on.
+struct Range {
+  int lo, hi, tail;
+  __device__ bool has(int i) const { return i >= lo && (i < hi || i >= tail); }
+};
+
+// Max and sum over aligned groups of n lanes, of which `mm` is this one's.
+__device__ __forceinline__ float lanes_max(float v, int n, unsigned mm) {
+  for (int o = n >> 1; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mm, v, o));
+  return v;
+}
+__device__ __forceinline__ float lanes_sum(float v, int n, unsigned mm) {
+  for (int o = n >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(mm, v, o);
+  return v;
+}
+
+// Loads the entries; the maximum and log-sum-exp of the teacher's logits over
+// those in use.
+template <typename T>
+__device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long r, const Teacher& tc,
+                                                    const T* x, const T* g, const Range& rg,
+                                                    int lane, int n, unsigned mm) {
+  TeacherHead th;
+  const float st = (float)a.s;
+  float out = 0.0f, m = NEG_INF;
+  for (int j = lane; j < a.k; j += n) {
+    const int id = a.ids[r * a.k + j];
+    const bool inside = id >= 0 && id < a.V;
+    const float t = inside ? a.tl[r * a.k + j] : NEG_INF;
+    if (id >= a.V) out = 1.0f;
+    tc.id[j] = inside ? id : -1;
+    tc.p[j] = t;
+    tc.x[j] = inside ? to_f32<T>(x[id]) : 0.0f;
+    if (a.add && g && inside && rg.has(id)) tc.old[j] = to_f32<T>(g[id]);
+    m = fmaxf(m, t);
+  }
+  th.malformed = lanes_max(out, n, mm) > 0.0f;
+  m = lanes_max(m, n, mm);
+  th.tm = m == NEG_INF ? 0.0f : m;
+  float s = 0.0f;
+  for (int j = lane; j < a.k; j += n)
+    if (tc.id[j] >= 0) s += expf((tc.p[j] - th.tm) * st);
+  s = lanes_sum(s, n, mm);
+  if (a.tlse) {
+    th.tlog = (float)((double)a.tlse[r] - (double)th.tm * a.s);
+    th.P = s * expf(-th.tlog);
+  } else {
+    th.tlog = logf(s);
+    th.P = s > 0.0f ? 1.0f : s;  // no entry with a probability: no loss, no gradient
+  }
+  return th;
+}
+
+// The entries' probabilities and, where `loss`, the position's loss.
+__device__ __forceinline__ void teacher_terms(const RowArgs& a, long long r, const Teacher& tc,
+                                              const TeacherHead& th, const Base& h, float S,
+                                              bool loss, int lane, int n, unsigned mm) {
+  const double logS = log_of_sum(S), m = base_score(h, a.sl);
+  float part = 0.0f;
+  for (int j = lane; j < a.k; j += n) {
+    float p = 0.0f;
+    if (tc.id[j] >= 0 && tc.p[j] != NEG_INF) {
+      const float lt = (float)((double)(tc.p[j] - th.tm) * a.s - (double)th.tlog);
+      p = expf(lt);
+      if (p != 0.0f) part += p * (lt - (float)(((double)tc.x[j] - m) * a.s - logS));
+    }
+    tc.p[j] = p;
+  }
+  __syncwarp(mm);
+  if (loss) {
+    part = lanes_sum(part, n, mm);
+    const double tau = 1.0 / a.s;
+    if (lane == 0) a.tok[r] = (float)(tau * tau * (double)part);
+  }
+}
+
+// The gradient at the teacher's labels within `rg`: the row's value there
+// less the entries' probabilities (the first of equal labels takes the sum
+// over them, in order).
+template <typename T>
+__device__ __forceinline__ void teacher_fix(const RowArgs& a, const Teacher& tc, T* g,
+                                            const Base& h, float scale, float cq, int lane, int n,
+                                            const Range& rg) {
+  for (int j = lane; j < a.k; j += n) {
+    const int id = tc.id[j];
+    if (id < 0 || !rg.has(id)) continue;
+    bool first = true;
+    float p = 0.0f;
+    for (int i = 0; i < a.k; ++i) {
+      if (tc.id[i] != id) continue;
+      if (i < j) first = false;
+      p += tc.p[i];
+    }
+    if (!first) continue;
+    float gv = based_exp(tc.x[j], a.sl, h) * scale - cq * p;
+    if (a.add) gv += tc.old[j];
+    g[id] = from_f32<T>(gv);
+  }
+}
+
+// ------------------------------------------------------------ vectors of a row
+template <typename T>
+constexpr int vec_of = 16 / (int)sizeof(T);  // elements of a 16-byte vector
+
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[4], const float*) {
+  v[0] = __uint_as_float(u.x);
+  v[1] = __uint_as_float(u.y);
+  v[2] = __uint_as_float(u.z);
+  v[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[8], const __nv_bfloat16*) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[8], const __half*) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[4], const float*) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                    __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[8], const __nv_bfloat16*) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[8], const __half*) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// How a row divides: `head` elements up to the first 16-byte boundary, nb
+// vectors, and the rest.  head + tail <= 2 VE - 2 elements are taken one by a
+// thread.
+struct Split {
+  int head, nb, edge;  // edge: head + tail
+};
+
+template <typename T>
+__device__ __forceinline__ Split split_row(const T* x, int V) {
+  constexpr int VE = vec_of<T>;
+  Split s;
+  const int off = (int)(reinterpret_cast<uintptr_t>(x) & 15) / (int)sizeof(T);
+  s.head = min(V, off ? VE - off : 0);
+  s.nb = (V - s.head) / VE;
+  s.edge = V - s.nb * VE;
+  return s;
+}
+
+// Element index of edge element i (0 <= i < edge).
+template <typename T>
+__device__ __forceinline__ int edge_index(const Split& s, int i) {
+  return i < s.head ? i : s.nb * vec_of<T> + i;
+}
+
+#include "loss_lanes.cuh"
+#include "loss_ring.cuh"
+#include "loss_wide.cuh"
+
+// ----------------------------------------------------------------- launches
+template <typename T, int MODE>
+cudaError_t rows_in_mode(const RowArgs& a, cudaStream_t st) {
+  cudaError_t e;
+  if (launch_lanes<T, MODE>(a, st, e)) return e;
+  if (launch_ring<T, MODE>(a, st, e)) return e;
+  return launch_wide<T, MODE>(a, st);
+}
+
+template <typename T>
+cudaError_t rows_of(int mode, const RowArgs& a, cudaStream_t st) {
+  switch (mode) {
+    case LM_LOGPROB: return rows_in_mode<T, LM_LOGPROB>(a, st);
+    case LM_POLICY: return rows_in_mode<T, LM_POLICY>(a, st);
+    case LM_PREFERENCE: return rows_in_mode<T, LM_PREFERENCE>(a, st);
+    case LM_SCALED: return rows_in_mode<T, LM_SCALED>(a, st);
+    default: return rows_in_mode<T, LM_DISTILL>(a, st);
+  }
+}
+
+}  // namespace
+}  // namespace semicrf

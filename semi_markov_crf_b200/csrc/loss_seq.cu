@@ -3,9 +3,8 @@
 // both (one score per segmentation).
 //
 //   loss_sums_kernel    one CTA per sequence: the float64 sums of the
-//                       per-position terms in a fixed order.  CTA 0 also looks
-//                       all lengths over and is the only writer of the status
-//                       word, so nothing has to clear it first.
+//                       per-position terms in a fixed order; a bad length goes
+//                       to the status word, which the row pass cleared.
 //   loss_pairs_kernel   one CTA per pair: S = sum of logp - ref of both
 //                       sequences (or its mean), the logistic loss on
 //                       u = beta (S_c - S_r) - margin, and the weight of each
@@ -39,13 +38,6 @@ __device__ __forceinline__ double cta_sum(double v, double* red) {
   return s;
 }
 
-__device__ __forceinline__ void report_lengths(const SeqArgs& a) {
-  int bad = 0;
-  for (int b = threadIdx.x; b < a.B; b += SUM_THREADS) bad |= a.lengths[b] < 0 || a.lengths[b] > a.T;
-  bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) *a.status = bad ? ST_BAD_LENGTH : 0;
-}
-
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
 
 // loss, d loss / d u of the smoothed logistic loss.
@@ -64,9 +56,9 @@ __device__ __forceinline__ void logistic(double u, double smoothing, double& los
 __global__ void __launch_bounds__(SUM_THREADS) loss_sums_kernel(SeqArgs a) {
   __shared__ double red[SUM_THREADS / 32];
   const int b = blockIdx.x, tid = threadIdx.x;
-  if (b == 0) report_lengths(a);
   const int L = a.lengths[b];
   const bool bad = L < 0 || L > a.T;
+  if (bad && tid == 0) set_status(a.status, ST_BAD_LENGTH);
   const int n = bad ? 0 : L;
   const long long row = (long long)b * a.T;
   double s = 0.0, k = 0.0, c = 0.0;
@@ -92,7 +84,6 @@ __global__ void __launch_bounds__(SUM_THREADS) loss_sums_kernel(SeqArgs a) {
 __global__ void __launch_bounds__(SUM_THREADS) loss_pairs_kernel(SeqArgs a) {
   __shared__ double red[SUM_THREADS / 32];
   const int i = blockIdx.x, P = a.B / 2, tid = threadIdx.x;
-  if (i == 0) report_lengths(a);
   double reward[2], inv[2];
   bool bad = false;
   for (int side = 0; side < 2; ++side) {
@@ -100,6 +91,7 @@ __global__ void __launch_bounds__(SUM_THREADS) loss_pairs_kernel(SeqArgs a) {
     const int L = a.lengths[b];
     const bool off = L < 0 || L > a.T;
     bad |= off;
+    if (off && tid == 0) set_status(a.status, ST_BAD_LENGTH);
     const int n = off ? 0 : L;
     const long long row = (long long)b * a.T;
     double s = 0.0, c = 0.0;

@@ -1,0 +1,112 @@
+// loss_wide.cuh -- rows too wide for the rings of a cluster: one CTA per row,
+// elements strided over its threads, the row read twice (included by loss_row.cuh).
+
+constexpr int WIDE_THREADS = 512;
+
+__device__ __forceinline__ float wide_max(float v, float* red) {
+  v = group_max(v, 32);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = NEG_INF;
+  for (int i = 0; i < WIDE_THREADS / 32; ++i) s = fmaxf(s, red[i]);
+  return s;
+}
+
+__device__ __forceinline__ float wide_sum(float v, float* red) {
+  v = group_sum(v, 32);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int i = 0; i < WIDE_THREADS / 32; ++i) s += red[i];
+  return s;
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_constant__ RowArgs a) {
+  __shared__ float red[WIDE_THREADS / 32];
+  __shared__ float tshare[2];
+  extern __shared__ float dyn[];
+  const long long r = blockIdx.x;
+  const int tid = threadIdx.x, V = a.V, warp = tid >> 5, lane = tid & 31;
+  if (r == 0 && tid == 0 && a.status) *a.status = 0;
+  const Head h = make_head<MODE>(a, load_head<MODE>(a, r));
+  const T* x = row_at<T>(a.x, r, a.ldx);
+  T* g = a.g ? row_at<T>(a.g, r, a.ldg) : nullptr;
+  const float w = MODE == LM_SCALED && h.live ? a.wseq[h.b] : 0.0f;
+  bool blank = !h.live || h.malformed || (MODE == LM_SCALED && w == 0.0f);
+  bool malformed = h.live;
+  const Range all{0, V, V};
+  Teacher tc{dyn, reinterpret_cast<int*>(dyn + a.k), dyn + 2 * a.k, dyn + 3 * a.k};
+  TeacherHead th{};
+  if (MODE == LM_DISTILL && h.live) {
+    if (warp == 0) {
+      th = teacher_head<T>(a, r, tc, x, g, all, lane, 32, FULL_MASK);
+      if (lane == 0) {
+        tshare[0] = th.P;
+        tshare[1] = th.malformed ? 1.0f : 0.0f;
+      }
+    }
+    __syncthreads();
+    blank = tshare[1] != 0.0f;
+  }
+  if (blank) {
+    if (MODE != LM_SCALED && tid == 0) blank_outputs<MODE>(a, r, malformed);
+    if (g && !a.add)
+      for (int v = tid; v < V; v += WIDE_THREADS) g[v] = from_f32<T>(0.0f);
+    return;
+  }
+
+  Base base;
+  float S, cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
+  if (MODE == LM_SCALED) {
+    base = unpack_stat(a.stat[r], S);
+    cy = (float)((double)w * a.s);
+    cq = -cy;
+  } else {
+    // maximum and sum of exponentials in one pass
+    float m = NEG_INF, s = 0.0f;
+    for (int v = tid; v < V; v += WIDE_THREADS) {
+      const float xv = to_f32<T>(x[v]);
+      if (xv > m) {
+        s *= ex2((m - xv) * a.sl);
+        m = xv;
+      }
+      s += ex2((xv - (m == NEG_INF ? 0.0f : m)) * a.sl);
+    }
+    const float M = wide_max(m, red);
+    S = wide_sum(m == NEG_INF && s == 0.0f ? 0.0f : s * ex2((m - M) * a.sl), red);
+    if (M == NEG_INF) S = quiet_nan();  // nothing but -inf: no distribution
+    base.at = M;
+    base.direct = false;
+    if (MODE == LM_DISTILL) {
+      P = tshare[0];
+      if (warp == 0) teacher_terms(a, r, tc, th, base, S, true, lane, 32, FULL_MASK);
+      cq = (float)((a.w ? a.w[h.b] : 1.0) / a.s);
+      if (a.add) __syncthreads();  // the gradient's old values at the entries are read
+    } else {
+      cy = label_outputs<MODE>(a, r, load_label<T, MODE>(a, r, h, x), base, S, tid == 0);
+      cq = -cy;
+    }
+  }
+  if (!g || MODE == LM_PREFERENCE) return;
+  const float scale = cq * P / S;
+  for (int v = tid; v < V; v += WIDE_THREADS) {
+    float gv = based_exp(to_f32<T>(x[v]), a.sl, base) * scale;
+    if (has_label(MODE) && v == h.y) gv += cy;
+    if (a.add) gv += to_f32<T>(g[v]);
+    g[v] = from_f32<T>(gv);
+  }
+  if (MODE == LM_DISTILL) {
+    __syncthreads();  // the row is written; its teacher entries follow
+    if (warp == 0) teacher_fix<T>(a, tc, g, base, scale, cq, lane, 32, all);
+  }
+}
+
+template <typename T, int MODE>
+cudaError_t launch_wide(const RowArgs& a, cudaStream_t st) {
+  const size_t smem = MODE == LM_DISTILL ? (size_t)TEACHER_WORDS * a.k * sizeof(float) : 0;
+  loss_wide_kernel<T, MODE><<<(unsigned)((long long)a.B * a.T), WIDE_THREADS, smem, st>>>(a);
+  return cudaGetLastError();
+}

@@ -30,7 +30,7 @@ KERNELS = ("prefix_reduce_kernel", "prefix_scan_kernel", "chain_exp_kernel", "ch
            "reduce_partials_kernel", "viterbi_kernel", "viterbi_pipe_kernel", "viterbi_argmax_kernel",
            "viterbi_words_kernel", "viterbi_walk_kernel", "path_terms_kernel", "path_grad_kernel",
            "proj_grad_kernel", "loss_rows_kernel", "loss_sums_kernel", "loss_pairs_kernel",
-           "loss_scaled_kernel", "policy_scores_kernel", "preference_scores_kernel")
+           "policy_scores_kernel", "preference_scores_kernel")
 
 FLAG_NO_CENTER = 0x1
 FLAG_FORWARD_ONLY = 0x2
