@@ -98,6 +98,23 @@ __device__ __forceinline__ void join_lanes(float& mb, float& s, int n) {
   mb = M;
 }
 
+// This thread's vectors of a chunk, -inf where the chunk ends before them.
+template <typename T>
+__device__ __forceinline__ void take_chunk(uint4 (&raw)[RING_NV], const uint4* chunk, int gt, int GT,
+                                           int have) {
+  if (have >= RING_NV * GT) {
+#pragma unroll
+    for (int i = 0; i < RING_NV; ++i) raw[i] = chunk[i * GT + gt];
+  } else {
+#pragma unroll
+    for (int i = 0; i < RING_NV; ++i) {
+      constexpr uint32_t none = Vec<T>::LOWEST;
+      raw[i] = make_uint4(none, none, none, none);
+      if (i * GT + gt < have) raw[i] = chunk[i * GT + gt];
+    }
+  }
+}
+
 template <typename T, int MODE, bool GRAD>
 __global__ void __launch_bounds__(RING_THREADS, 1)
     loss_ring_kernel(const __grid_constant__ RowArgs a, const RingShape shape) {
@@ -283,31 +300,27 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
         if (!dead && !mbar_wait(&full[cur.slot], cur.phase, WAIT_SPIN_LIMIT)) gave_up();
         const uint4* chunk =
             reinterpret_cast<const uint4*>(ring + (size_t)cur.slot * W * RING_WARP_BYTES);
-        const int have = n - c * chunk_vecs;
-        float v[RING_NV][VE];
-        float top = NEG_INF;
-#pragma unroll
-        for (int i = 0; i < RING_NV; ++i) {
-          if (i * GT + gt < have) {
-            unpack(chunk[i * GT + gt], v[i], x);
-          } else {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) v[i][e] = NEG_INF;
-          }
-#pragma unroll
-          for (int e = 0; e < VE; ++e) top = fmaxf(top, v[i][e]);
-        }
+        uint4 raw[RING_NV];
+        take_chunk<T>(raw, chunk, gt, GT, n - c * chunk_vecs);
         if (!GRAD) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[cur.slot]);
         }
-        const float nb = fmaxf(mb, top * a.sl);
+        const float nb = fmaxf(mb, Vec<T>::greatest(raw) * a.sl);
         const float at = nb == NEG_INF ? 0.0f : nb;  // nothing above -inf yet: exponentials of 0
-        float sum = 0.0f;
+        const f32x2 sl2 = pair(a.sl, a.sl), at2 = pair(-at, -at);
+        f32x2 sum2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
-        for (int i = 0; i < RING_NV; ++i)
+        for (int i = 0; i < RING_NV; ++i) {
+          f32x2 v[Vec<T>::PAIRS];
+          Vec<T>::unpack(raw[i], v);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) sum += ex2(fmaf(v[i][e], a.sl, -at));
+          for (int e = 0; e < Vec<T>::PAIRS; ++e)
+            sum2[e & 1] = add2(sum2[e & 1], ex2_2(fma2(v[e], sl2, at2)));
+        }
+        float sum, odd;
+        halves(add2(sum2[0], sum2[1]), sum, odd);
+        sum += odd;
         s = (mb == NEG_INF && s == 0.0f ? 0.0f : s * ex2(mb - nb)) + sum;
         mb = nb;
         cur.next(slots);
@@ -400,42 +413,45 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
       const uint4* chunk =
           reinterpret_cast<const uint4*>(ring + (size_t)cur.slot * W * RING_WARP_BYTES);
       const int have = n - c * chunk_vecs;
-      float v[RING_NV][VE];
-#pragma unroll
-      for (int i = 0; i < RING_NV; ++i)
-        if (i * GT + gt < have) unpack(chunk[i * GT + gt], v[i], x);
+      uint4 raw[RING_NV];
+      take_chunk<T>(raw, chunk, gt, GT, have);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[cur.slot]);
-      if (base.direct) {
-#pragma unroll
-        for (int i = 0; i < RING_NV; ++i)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) v[i][e] = ex2(fmaf(v[i][e], a.sl, -base.at)) * scale;
-      } else {
-#pragma unroll
-        for (int i = 0; i < RING_NV; ++i)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) v[i][e] = ex2((v[i][e] - base.at) * a.sl) * scale;
-      }
-      if (MODE == LM_DISTILL && blank) {
-#pragma unroll
-        for (int i = 0; i < RING_NV; ++i)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) v[i][e] = 0.0f;
-      }
 #pragma unroll
       for (int i = 0; i < RING_NV; ++i) {
-        if (i * GT + gt >= have) continue;
+        if (i * GT + gt >= have) break;
         const size_t slot = (size_t)c * chunk_vecs + i * GT + gt;
-        if (sizeof(T) == 4 && a.add) {
+        f32x2 v[Vec<T>::PAIRS];
+        Vec<T>::unpack(raw[i], v);
+        if (base.direct) {
+          const f32x2 sl2 = pair(a.sl, a.sl), at2 = pair(-base.at, -base.at),
+                      scale2 = pair(scale, scale);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) v[i][e] += to_f32<T>(gb[slot * VE + e]);
-        }
-        if (same) {
-          reinterpret_cast<uint4*>(gb)[slot] = pack(v[i], x);
+          for (int e = 0; e < Vec<T>::PAIRS; ++e) v[e] = mul2(ex2_2(fma2(v[e], sl2, at2)), scale2);
         } else {
 #pragma unroll
-          for (int e = 0; e < VE; ++e) gb[slot * VE + e] = from_f32<T>(v[i][e]);
+          for (int e = 0; e < Vec<T>::PAIRS; ++e) {
+            float lo, hi;
+            halves(v[e], lo, hi);
+            v[e] = pair(based_exp(lo, a.sl, base) * scale, based_exp(hi, a.sl, base) * scale);
+          }
+        }
+        if (MODE == LM_DISTILL && blank) {
+#pragma unroll
+          for (int e = 0; e < Vec<T>::PAIRS; ++e) v[e] = pair(0.0f, 0.0f);
+        }
+        if (sizeof(T) == 4 && a.add) {
+#pragma unroll
+          for (int e = 0; e < Vec<T>::PAIRS; ++e)
+            v[e] = add2(v[e], pair(to_f32<T>(gb[slot * VE + 2 * e]), to_f32<T>(gb[slot * VE + 2 * e + 1])));
+        }
+        const uint4 q = Vec<T>::pack(v);
+        if (same) {
+          reinterpret_cast<uint4*>(gb)[slot] = q;
+        } else {
+          const T* each = reinterpret_cast<const T*>(&q);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) gb[slot * VE + e] = each[e];
         }
       }
       cur.next(slots);

@@ -326,51 +326,138 @@ __device__ __forceinline__ void teacher_fix(const RowArgs& a, const Teacher& tc,
 template <typename T>
 constexpr int vec_of = 16 / (int)sizeof(T);  // elements of a 16-byte vector
 
-__device__ __forceinline__ void unpack(const uint4& u, float (&v)[4], const float*) {
-  v[0] = __uint_as_float(u.x);
-  v[1] = __uint_as_float(u.y);
-  v[2] = __uint_as_float(u.z);
-  v[3] = __uint_as_float(u.w);
+// Two float32 in one 64-bit register pair: a fused multiply-add, an addition
+// or a multiplication of both is one instruction on sm_100.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
 }
-__device__ __forceinline__ void unpack(const uint4& u, float (&v)[8], const __nv_bfloat16*) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+__device__ __forceinline__ void halves(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
+  float lo, hi;
+  halves(v, lo, hi);
+  return pair(ex2(lo), ex2(hi));
+}
+
+// A 16-byte vector of T as pairs of float32, its greatest element, -inf, and back.
+template <typename T>
+struct Vec;
+
+template <>
+struct Vec<float> {
+  static constexpr int PAIRS = 2;
+  static constexpr uint32_t LOWEST = 0xff800000u;  // -inf
+  static __device__ __forceinline__ void unpack(const uint4& u, f32x2 (&v)[2]) {
+    v[0] = pair(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[1] = pair(__uint_as_float(u.z), __uint_as_float(u.w));
   }
-}
-__device__ __forceinline__ void unpack(const uint4& u, float (&v)[8], const __half*) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+  static __device__ __forceinline__ uint4 pack(const f32x2 (&v)[2]) {
+    float a, b, c, d;
+    halves(v[0], a, b);
+    halves(v[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
   }
-}
-__device__ __forceinline__ uint4 pack(const float (&v)[4], const float*) {
-  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                    __float_as_uint(v[3]));
-}
-__device__ __forceinline__ uint4 pack(const float (&v)[8], const __nv_bfloat16*) {
-  uint32_t w[4];
+  template <int N>
+  static __device__ __forceinline__ float greatest(const uint4 (&u)[N]) {
+    float m[2] = {NEG_INF, NEG_INF};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < N; ++i) {
+      m[0] = fmaxf(m[0], fmaxf(__uint_as_float(u[i].x), __uint_as_float(u[i].y)));
+      m[1] = fmaxf(m[1], fmaxf(__uint_as_float(u[i].z), __uint_as_float(u[i].w)));
+    }
+    return fmaxf(m[0], m[1]);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint4 pack(const float (&v)[8], const __half*) {
-  uint32_t w[4];
+};
+
+// Both 16-bit types: elements 2i and 2i + 1 share a word.
+template <typename H, typename H2>
+struct Vec16 {
+  static constexpr int PAIRS = 4;
+  template <int N>
+  static __device__ __forceinline__ float greatest(const uint4 (&u)[N]) {
+    H2 m[4];
+    const uint4 first = u[0];
+    m[0] = *reinterpret_cast<const H2*>(&first.x);
+    m[1] = *reinterpret_cast<const H2*>(&first.y);
+    m[2] = *reinterpret_cast<const H2*>(&first.z);
+    m[3] = *reinterpret_cast<const H2*>(&first.w);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 1; i < N; ++i) {
+      const uint4 q = u[i];
+      m[0] = __hmax2(m[0], *reinterpret_cast<const H2*>(&q.x));
+      m[1] = __hmax2(m[1], *reinterpret_cast<const H2*>(&q.y));
+      m[2] = __hmax2(m[2], *reinterpret_cast<const H2*>(&q.z));
+      m[3] = __hmax2(m[3], *reinterpret_cast<const H2*>(&q.w));
+    }
+    const H2 t = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+    return fmaxf(to_f32<H>(t.x), to_f32<H>(t.y));
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+};
+
+template <>
+struct Vec<__nv_bfloat16> : Vec16<__nv_bfloat16, __nv_bfloat162> {
+  static constexpr uint32_t LOWEST = 0xff80ff80u;  // -inf twice
+  static __device__ __forceinline__ void unpack(const uint4& u, f32x2 (&v)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 pack(const f32x2 (&v)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      halves(v[i], lo, hi);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+template <>
+struct Vec<__half> : Vec16<__half, __half2> {
+  static constexpr uint32_t LOWEST = 0xfc00fc00u;
+  static __device__ __forceinline__ void unpack(const uint4& u, f32x2 (&v)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[i] = pair(f.x, f.y);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const f32x2 (&v)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      halves(v[i], lo, hi);
+      const __half2 h = __floats2half2_rn(lo, hi);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
 
 // How a row divides: `head` elements up to the first 16-byte boundary, nb
 // vectors, and the rest.  head + tail <= 2 VE - 2 elements are taken one by a
