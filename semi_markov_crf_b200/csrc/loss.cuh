@@ -30,6 +30,7 @@ struct RowArgs {
   const int32_t* labels;  // [B, T], negative: does not count (not for LM_DISTILL)
   float sl;             // log2(e) / temperature
   double s;             // 1 / temperature
+  double inv_sl;        // 1 / sl
   const float* grad_logp;  // LM_LOGPROB: d loss / d logp [B, T] (nullptr: ones)
   const float* old_logp;   // LM_POLICY
   const float* ref_logp;   // LM_POLICY, LM_PREFERENCE; nullptr: no reference

@@ -83,6 +83,7 @@ int prepare_rows(const void* logits, int dtype, int64_t ld, const int32_t* lengt
   a.lengths = lengths;
   a.s = 1.0 / temperature;
   a.sl = (float)(LOG2E_D / temperature);
+  a.inv_sl = 1.0 / (double)a.sl;
   a.status = p.status;
   return SEMICRF_OK;
 }

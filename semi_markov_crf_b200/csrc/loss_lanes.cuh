@@ -29,16 +29,20 @@ __global__ void __launch_bounds__(LANES_THREADS) loss_lanes_kernel(
     return;
   }
 
+  TeacherAhead ahead;
+  if (MODE == LM_DISTILL) ahead.load(a, r, 0, lane, L);
   float v[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) v[i] = i * L + lane < V ? to_f32<T>(x[i * L + lane]) : NEG_INF;
-  const LabelIn in = load_label<T, MODE>(a, r, h, x);
+  const LabelIn<T> in = load_label<T, MODE>(a, r, h, x);
   const Range all{0, V, V};
-  float* mine = dyn + (size_t)(tid / L) * (MODE == LM_DISTILL ? TEACHER_WORDS * a.k : 0);
-  Teacher tc{mine, reinterpret_cast<int*>(mine + a.k), mine + 2 * a.k, mine + 3 * a.k};
+  float* mine =
+      dyn + (size_t)(tid / L) * (MODE == LM_DISTILL ? TEACHER_WORDS * a.k + teacher_table(a.k) : 0);
+  Teacher tc{mine, reinterpret_cast<int*>(mine + a.k), mine + 2 * a.k, mine + 3 * a.k,
+             reinterpret_cast<int*>(mine + TEACHER_WORDS * a.k)};
   TeacherHead th{};
   if (MODE == LM_DISTILL) {
-    th = teacher_head<T>(a, r, tc, x, g, all, lane, L, mm);
+    th = teacher_head<T>(a, r, tc, ahead, x, g, all, lane, L, mm);
     if (th.malformed) {
       if (lane == 0) blank_outputs<MODE>(a, r, true);
       if (g && !a.add)
@@ -92,7 +96,7 @@ __global__ void __launch_bounds__(LANES_THREADS) loss_lanes_kernel(
   }
   if (MODE == LM_DISTILL) {
     __syncwarp(mm);  // the row is written; its teacher entries follow
-    teacher_fix<T>(a, tc, g, base, scale, cq, lane, L, all);
+    teacher_fix<T>(a, tc, g, base, scale, cq, th.repeats, lane, L, all);
   }
 }
 
@@ -102,7 +106,7 @@ cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
   int threads = LANES_THREADS;
   size_t smem = 0;
   if (MODE == LM_DISTILL) {
-    const size_t row = (size_t)TEACHER_WORDS * a.k * sizeof(float);
+    const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float);
     while (threads > 32 && threads / L * row > 48 * 1024) threads /= 2;
     smem = threads / L * row;
   }
@@ -120,7 +124,8 @@ bool launch_lanes(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   int L = V <= 8 ? 1 : V <= 16 ? 2 : V <= 32 ? 4 : V <= 64 ? 8 : V <= 128 ? 16 : 32;
   if (V > 256) return false;
   if (MODE == LM_DISTILL)
-    while (L < 32 && 32 / L * TEACHER_WORDS * a.k * sizeof(float) > 48 * 1024) L *= 2;
+    while (L < 32 && 32 / L * (TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float) > 48 * 1024)
+      L *= 2;
   switch (L) {
     case 1: e = launch_lanes_shape<T, MODE, 1, 8>(a, st); break;
     case 2: e = launch_lanes_shape<T, MODE, 2, 8>(a, st); break;

@@ -1,31 +1,37 @@
-// loss_ring.cuh -- long rows: persistent CTAs that stream rows through a ring
-// of shared-memory chunks (included by loss_row.cuh).
+// loss_ring.cuh -- long rows: persistent CTAs that stream rows through rings of
+// shared-memory chunks (included by loss_row.cuh).
 //
-// A CTA has 16 consumer warps, divided into groups of W warps, and one warp
-// that only issues copies.  Each group has a ring of its own and works on a
-// row at a time:
-//   pass 1  as its chunks arrive (TMA bulk copies, one mbarrier a chunk), the
-//           running maximum and sum of exponentials;
-//   join    the group's warps (and, for rows wider than one ring, the CTAs of
-//           a cluster, through distributed shared memory) exchange (maximum,
-//           sum); the position's terms follow;
-//   pass 2  the gradient from the same chunks, still in shared memory, which
-//           gives each back to the ring.
-// A row is read from memory once, and the next row's chunks arrive while this
-// one is joined and written.  Without a gradient a chunk goes back after pass
-// 1, and the second pass of the preference loss (LM_SCALED) runs pass 2 alone.
+// The warps of a CTA have roles, and pass rows on to one another through
+// mbarriers, so that copies, both passes and a position's scalar work overlap:
+//   copier    (one warp)  issues the TMA bulk copies of every group's ring;
+//   reducers  take each chunk as it arrives: running maximum and sum of
+//             exponentials;
+//   scalar    (one warp a group) joins the reducers' pairs (and, for a row wider
+//             than a ring, those of the CTAs of a cluster, through distributed
+//             shared memory), computes the position's terms, looks after the
+//             teacher's entries and the row's unaligned ends, and publishes what
+//             the writers need;
+//   writers   compute the gradient from the same chunks, still in shared
+//             memory, and give them back to the ring.
+// A row is read from memory once.  While its gradient is written the next row
+// arrives and is reduced.  Without a gradient all warps reduce; in the second
+// pass of the preference loss (LM_SCALED) all of them write.
 //
-// Every wait is bounded: a wait that gives up records ST_DEVICE_TIMEOUT in the
-// status word and the kernel runs on without waiting (every access stays
-// within the rows and the ring), so that it ends.
+// The 16 reducing and writing warps form groups of W, each with a ring of its
+// own and a row at a time: short rows need several rows in flight.
+//
+// Every wait is bounded: one that gives up records ST_DEVICE_TIMEOUT in the
+// status word, and its thread runs on without waiting (every access stays
+// within the rows and the rings), so that the kernel ends.
 
-constexpr int RING_WARPS = 16;                        // consumer warps of a CTA
-constexpr int RING_THREADS = (RING_WARPS + 1) * 32;   // and the copying warp
-constexpr int RING_NV = 4;                            // vectors of a chunk a thread takes
-constexpr int RING_WARP_BYTES = RING_NV * 32 * 16;    // a warp's part of a chunk
-constexpr int RING_SLOTS_MAX = 16;                    // chunks of a group's ring
+constexpr int RING_WARPS = 16;                      // reducers and writers of a CTA
+constexpr int RING_GROUPS = 8;                      // at most
+constexpr int RING_THREADS = (RING_WARPS + RING_GROUPS + 1) * 32;  // at most
+constexpr int RING_NV = 4;                          // vectors of a chunk a thread takes
+constexpr int RING_WARP_BYTES = RING_NV * 32 * 16;  // a warp's part of a chunk
+constexpr int RING_SLOTS_MAX = 16;                  // chunks of a group's ring
 constexpr int RING_CLUSTER_MAX = 8;
-constexpr int RING_SMEM = 220 * 1024;
+constexpr int RING_SMEM = 224 * 1024;
 
 struct RingShape {
   int W;      // warps of a group
@@ -33,13 +39,20 @@ struct RingShape {
   int cl;     // CTAs that share a row
 };
 
-struct RingBars {
-  uint64_t full[RING_WARPS * RING_SLOTS_MAX];
-  uint64_t empty[RING_WARPS * RING_SLOTS_MAX];
-  uint64_t peer[2];
+// What the scalar warp tells the writers about a row.
+struct RowNote {
+  float at, scale, cy, gy;  // base, factor of the exponentials, addend and value at the label
+  int y;                    // the label (-1: none)
+  int kind;                 // NOTE_*
+};
+constexpr int NOTE_DIRECT = 0, NOTE_DIFFERENCE = 1, NOTE_ZERO = 2;
+
+struct GroupState {
+  uint64_t full[RING_SLOTS_MAX], empty[RING_SLOTS_MAX];
+  uint64_t red_full[2], red_free[2], note_full[2], note_free[2], peer[2];
   float2 red[2][RING_WARPS];
   float2 part[2][RING_CLUSTER_MAX];
-  float tshare[2][RING_WARPS][2];
+  RowNote note[2];
 };
 
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
@@ -70,6 +83,29 @@ struct Cursor {
   }
 };
 
+// Rows alternate between two sets of barriers and slots: which, and its parity.
+struct Turn {
+  int i;
+  uint32_t phase;
+  __device__ void next() {
+    phase ^= (uint32_t)i;
+    i ^= 1;
+  }
+};
+
+// Waits that give up once and for all.
+struct Waiter {
+  int* status;
+  bool dead;
+  __device__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (!dead && !mbar_wait(bar, parity, WAIT_SPIN_LIMIT)) give_up();
+  }
+  __device__ void give_up() {
+    dead = true;
+    if (status) set_status(status, ST_DEVICE_TIMEOUT);
+  }
+};
+
 // The vectors of row x that CTA `rank` of `cl` takes.
 struct Part {
   Split sp;
@@ -79,22 +115,55 @@ template <typename T>
 __device__ __forceinline__ Part part_of(const T* x, int V, int rank, int cl) {
   Part p;
   p.sp = split_row(x, V);
-  const int per = (p.sp.nb + cl - 1) / cl;
-  p.lo = min(rank * per, p.sp.nb);
-  p.n = min(per, p.sp.nb - p.lo);
+  if (cl == 1) {
+    p.lo = 0;
+    p.n = p.sp.nb;
+  } else {
+    const int per = (p.sp.nb + cl - 1) / cl;
+    p.lo = min(rank * per, p.sp.nb);
+    p.n = min(per, p.sp.nb - p.lo);
+  }
   return p;
 }
 
-// Rows whose weight is 0 get a zero gradient without being read.
+// Heads of a unit's rows, loaded a row ahead.
 template <int MODE>
-__device__ __forceinline__ bool row_blank(const Head& h, float w) {
-  return !h.live || h.malformed || (MODE == LM_SCALED && w == 0.0f);
+struct HeadStream {
+  HeadLoad next;
+  float next_w;
+  __device__ void load(const RowArgs& a, int r, int rows) {
+    if (r >= rows) return;
+    next = load_head<MODE>(a, r);
+    if (MODE == LM_SCALED) next_w = a.wseq[next.b];
+  }
+  // Rows that do not count, and rows of weight 0, are not read.
+  __device__ Head take(const RowArgs& a, float& w, bool& blank) const {
+    const Head h = make_head<MODE>(a, next);
+    w = next_w;
+    blank = !h.live || h.malformed || (MODE == LM_SCALED && w == 0.0f);
+    return h;
+  }
+};
+
+// Maximum over a warp (a NaN is ignored, as fmaxf does).
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 
 // Maximum and sum of a warp's (base, sum) pairs; -inf beside 0 is nothing.
-__device__ __forceinline__ void join_lanes(float& mb, float& s, int n) {
-  const float M = lanes_max(mb, n, FULL_MASK);
-  s = lanes_sum(mb == NEG_INF && s == 0.0f ? 0.0f : s * ex2(mb - M), n, FULL_MASK);
+__device__ __forceinline__ void join_lanes(float& mb, float& s) {
+  const float M = warp_max(mb);
+  s = group_sum(mb == NEG_INF && s == 0.0f ? 0.0f : s * ex2(mb - M), 32);
+  mb = M;
+}
+
+// One more (base, sum) pair.
+__device__ __forceinline__ void join_pair(float& mb, float& s, float mb2, float s2) {
+  const float M = fmaxf(mb, mb2);
+  s = (mb == NEG_INF && s == 0.0f ? 0.0f : s * ex2(mb - M)) +
+      (mb2 == NEG_INF && s2 == 0.0f ? 0.0f : s2 * ex2(mb2 - M));
   mb = M;
 }
 
@@ -115,373 +184,498 @@ __device__ __forceinline__ void take_chunk(uint4 (&raw)[RING_NV], const uint4* c
   }
 }
 
+// What a role's loop over rows needs.
+struct RingPlace {
+  unsigned char* ring;
+  GroupState* st;
+  int first, units, rows;  // this group's rows: first, first + units, ...
+  int rank, cl, slots, chunk_bytes;
+};
+
+// ---------------------------------------------------------------------- copier
+template <typename T, int MODE>
+__device__ __forceinline__ void ring_copier(const RowArgs& a, unsigned char* rings, GroupState* states,
+                                            int groups, size_t ring_bytes, const RingPlace& pl,
+                                            int lane) {
+  const bool mine = lane < groups;
+  unsigned char* ring = rings + (mine ? lane : 0) * ring_bytes;
+  GroupState& st = states[mine ? lane : 0];
+  int r = pl.first + lane;
+  bool done = !mine || r >= pl.rows, open = false;
+  HeadStream<MODE> heads{};
+  if (!done) heads.load(a, r, pl.rows);
+  Cursor cur{0, 0};
+  const unsigned char* src = nullptr;
+  int left = 0, idle = 0;
+  while (!__all_sync(FULL_MASK, done)) {
+    bool moved = false;
+    if (!done && !open) {
+      if (r >= pl.rows) {
+        done = true;
+      } else {
+        float w;
+        bool blank;
+        heads.take(a, w, blank);
+        if (!blank) {
+          const T* x = row_at<T>(a.x, r, a.ldx);
+          const Part p = part_of(x, a.V, pl.rank, pl.cl);
+          src = reinterpret_cast<const unsigned char*>(x + p.sp.head) + (size_t)p.lo * 16;
+          left = p.n * 16;
+          open = left > 0;
+        }
+        r += pl.units;
+        heads.load(a, r, pl.rows);
+      }
+      moved = true;
+    } else if (open && mbar_test(&st.empty[cur.slot], cur.phase ^ 1)) {
+      const int n = min(left, pl.chunk_bytes);
+      mbar_expect_tx(&st.full[cur.slot], n);
+      bulk_g2s(ring + (size_t)cur.slot * pl.chunk_bytes, src, n, &st.full[cur.slot]);
+      src += n;
+      left -= n;
+      open = left > 0;
+      cur.next(pl.slots);
+      moved = true;
+    }
+    if (__any_sync(FULL_MASK, moved)) {
+      idle = 0;
+    } else {
+      __nanosleep(100);
+      if (++idle >= WAIT_SPIN_LIMIT) {
+        if (lane == 0 && a.status) set_status(a.status, ST_DEVICE_TIMEOUT);
+        break;
+      }
+    }
+  }
+  // The CTA's shared memory outlives its copies: wait for those still in flight.
+  // A slot's last copy is of this pass over the ring or of the one before (a
+  // barrier that was never used counts as past that one).
+  if (mine)
+    for (int i = 0; i < pl.slots; ++i)
+      mbar_wait(&st.full[i], i < cur.slot ? cur.phase : cur.phase ^ 1, WAIT_SPIN_LIMIT);
+}
+
+// -------------------------------------------------------------------- reducers
+// GT threads, this one gt.  RELEASE: nobody else needs the chunks.
+template <typename T, int MODE, bool RELEASE>
+__device__ __forceinline__ void ring_reduce(const RowArgs& a, const RingPlace& pl, int gt, int GT) {
+  GroupState& st = *pl.st;
+  const int lane = gt & 31, gw = gt >> 5, chunk_vecs = pl.chunk_bytes / 16;
+  Waiter wait{a.status, false};
+  Cursor cur{0, 0};
+  Turn turn{0, 0};
+  HeadStream<MODE> heads{};
+  heads.load(a, pl.first, pl.rows);
+  const f32x2 sl2 = pair(a.sl, a.sl);
+  for (int r = pl.first; r < pl.rows; r += pl.units) {
+    float w;
+    bool blank;
+    heads.take(a, w, blank);
+    heads.load(a, r + pl.units, pl.rows);
+    if (blank) continue;
+    const int n = part_of(row_at<T>(a.x, r, a.ldx), a.V, pl.rank, pl.cl).n;
+    float mb = NEG_INF, s = 0.0f;
+    for (int c = 0; c < n; c += chunk_vecs) {
+      wait(&st.full[cur.slot], cur.phase);
+      uint4 raw[RING_NV];
+      take_chunk<T>(raw, reinterpret_cast<const uint4*>(pl.ring + (size_t)cur.slot * pl.chunk_bytes),
+                    gt, GT, n - c);
+      if (RELEASE) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st.empty[cur.slot]);
+      }
+      cur.next(pl.slots);
+      const float nb = fmaxf(mb, Vec<T>::greatest(raw) * a.sl);
+      const float at = nb == NEG_INF ? 0.0f : nb;  // nothing above -inf yet: exponentials of 0
+      const f32x2 at2 = pair(-at, -at);
+      f32x2 sum2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+#pragma unroll
+      for (int i = 0; i < RING_NV; ++i) {
+        f32x2 v[Vec<T>::PAIRS];
+        Vec<T>::unpack(raw[i], v);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::PAIRS; ++e)
+          sum2[e & 1] = add2(sum2[e & 1], ex2_of_pair<T>(fma2(v[e], sl2, at2), e));
+      }
+      float sum, odd;
+      halves(add2(sum2[0], sum2[1]), sum, odd);
+      s = (mb == NEG_INF && s == 0.0f ? 0.0f : s * ex2(mb - nb)) + (sum + odd);
+      mb = nb;
+    }
+    join_lanes(mb, s);
+    wait(&st.red_free[turn.i], turn.phase ^ 1);
+    if (lane == 0) {
+      st.red[turn.i][gw] = make_float2(mb, s);
+      mbar_arrive(&st.red_full[turn.i]);
+    }
+    turn.next();
+  }
+}
+
+// ---------------------------------------------------------------------- writers
+template <typename T, int MODE>
+__device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl, int gt, int GT) {
+  constexpr int VE = vec_of<T>;
+  GroupState& st = *pl.st;
+  const int lane = gt & 31, chunk_vecs = pl.chunk_bytes / 16;
+  Waiter wait{a.status, false};
+  Cursor cur{0, 0};
+  Turn turn{0, 0};
+  const f32x2 sl2 = pair(a.sl, a.sl);
+  for (int r = pl.first; r < pl.rows; r += pl.units) {
+    const T* x = row_at<T>(a.x, r, a.ldx);
+    T* g = row_at<T>(a.g, r, a.ldg);
+    const Part p = part_of(x, a.V, pl.rank, pl.cl);
+    // gradient rows of another alignment are stored element by element
+    const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(g)) & 15) == 0;
+    T* gb = g + p.sp.head + (size_t)p.lo * VE;
+    wait(&st.note_full[turn.i], turn.phase);
+    const RowNote note = st.note[turn.i];
+    if (note.kind == NOTE_ZERO && note.y < 0) {  // not read: zeros, unless added to
+      if (!a.add) {
+        for (int i = gt; i < p.n; i += GT) {
+          if (same) {
+            reinterpret_cast<uint4*>(gb)[i] = make_uint4(0, 0, 0, 0);
+          } else {
+            for (int e = 0; e < VE; ++e) gb[(size_t)i * VE + e] = from_f32<T>(0.0f);
+          }
+        }
+      }
+    } else {
+      const f32x2 at2 = pair(-note.at, -note.at), scale2 = pair(note.scale, note.scale);
+      const bool plain = note.kind == NOTE_DIRECT && same && !a.add;
+      for (int c = 0; c < p.n; c += chunk_vecs) {
+        wait(&st.full[cur.slot], cur.phase);
+        const uint4* chunk =
+            reinterpret_cast<const uint4*>(pl.ring + (size_t)cur.slot * pl.chunk_bytes);
+        const int have = p.n - c;
+        if (plain) {
+          uint4 raw[RING_NV];
+          take_chunk<T>(raw, chunk, gt, GT, have);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&st.empty[cur.slot]);
+#pragma unroll
+          for (int i = 0; i < RING_NV; ++i) {
+            f32x2 v[Vec<T>::PAIRS];
+            Vec<T>::unpack(raw[i], v);
+#pragma unroll
+            for (int e = 0; e < Vec<T>::PAIRS; ++e)
+              v[e] = mul2(ex2_of_pair<T>(fma2(v[e], sl2, at2), e), scale2);
+            raw[i] = Vec<T>::pack(v);
+          }
+          uint4* out = reinterpret_cast<uint4*>(gb) + c + gt;
+          if (have >= chunk_vecs) {
+#pragma unroll
+            for (int i = 0; i < RING_NV; ++i) out[i * GT] = raw[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < RING_NV; ++i)
+              if (i * GT + gt < have) out[i * GT] = raw[i];
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < RING_NV; ++i) {
+            const int at = i * GT + gt;
+            if (at >= have) break;
+            const T* each = reinterpret_cast<const T*>(chunk + at);
+            T* to = gb + (size_t)(c + at) * VE;
+#pragma unroll 1
+            for (int e = 0; e < VE; ++e) {
+              float gv = 0.0f;
+              if (note.kind == NOTE_DIRECT) gv = ex2(fmaf(to_f32<T>(each[e]), a.sl, -note.at)) * note.scale;
+              if (note.kind == NOTE_DIFFERENCE) gv = ex2((to_f32<T>(each[e]) - note.at) * a.sl) * note.scale;
+              if (a.add) gv += to_f32<T>(to[e]);
+              to[e] = from_f32<T>(gv);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&st.empty[cur.slot]);
+        }
+        cur.next(pl.slots);
+      }
+      if (has_label(MODE)) {
+        // the thread that wrote the label's element puts it right
+        const int at = note.y - p.sp.head - p.lo * VE;
+        if (at >= 0 && at < p.n * VE && at / VE % GT == gt)
+          g[note.y] = from_f32<T>(a.add ? to_f32<T>(g[note.y]) + note.cy : note.gy);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&st.note_free[turn.i]);
+    turn.next();
+  }
+}
+
+// ----------------------------------------------------------------- scalar warp
+template <typename T, int MODE, bool GRAD>
+__device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& pl, float* teachers,
+                                            int warps, int lane) {
+  constexpr int VE = vec_of<T>;
+  constexpr bool PASS1 = MODE != LM_SCALED;
+  GroupState& st = *pl.st;
+  Waiter wait{a.status, false};
+  Turn turn{0, 0}, rows_read{0, 0};
+  HeadStream<MODE> heads{};
+  heads.load(a, pl.first, pl.rows);
+  // the row whose teacher entries still have to be put into its gradient
+  bool due = false, due_repeats = false;
+  Base due_base{};
+  float due_scale = 0.0f, due_cq = 0.0f;
+  int due_row = 0;
+  Range due_range{};
+  const int tw = MODE == LM_DISTILL ? TEACHER_WORDS * a.k : 0;
+  auto teacher_at = [&](int i) {
+    float* t = teachers + i * tw;
+    return Teacher{t, reinterpret_cast<int*>(t + a.k), t + 2 * a.k, t + 3 * a.k,
+                   reinterpret_cast<int*>(teachers + 2 * tw)};
+  };
+  auto settle = [&](const Turn& then) {
+    // the writers are done with the row before this one
+    wait(&st.note_free[then.i], then.phase);
+    teacher_fix<T>(a, teacher_at(then.i), row_at<T>(a.g, due_row, a.ldg), due_base, due_scale, due_cq,
+                   due_repeats, lane, 32, due_range);
+    due = false;
+  };
+  TeacherAhead ahead{};
+  int ahead_row = -1;  // the row that `ahead` is of
+  for (int r = pl.first; r < pl.rows; r += pl.units) {
+    float w;
+    bool blank;
+    const Head h = heads.take(a, w, blank);
+    heads.load(a, r + pl.units, pl.rows);
+    const T* x = row_at<T>(a.x, r, a.ldx);
+    T* g = GRAD ? row_at<T>(a.g, r, a.ldg) : nullptr;
+    const Part p = part_of(x, a.V, pl.rank, pl.cl);
+    const int ei = pl.rank == 0 && lane < p.sp.edge ? edge_index<T>(p.sp, lane) : -1;
+    RowNote note{};
+    note.kind = NOTE_ZERO;
+    note.y = -1;
+    const Turn now = turn;
+    if (blank) {
+      if (PASS1 && pl.rank == 0 && lane == 0) blank_outputs<MODE>(a, r, h.live);
+      if (GRAD && !a.add && ei >= 0) g[ei] = from_f32<T>(0.0f);
+    } else {
+      const LabelIn<T> in = load_label<T, MODE>(a, r, h, x);
+      T xe = from_f32<T>(0.0f);
+      if (ei >= 0) xe = x[ei];
+      const Range rg = pl.rank == 0
+                           ? Range{0, p.sp.head + p.n * VE, p.sp.head + p.sp.nb * VE}
+                           : Range{p.sp.head + p.lo * VE, p.sp.head + (p.lo + p.n) * VE, a.V};
+      const Teacher tc = teacher_at(now.i);
+      TeacherHead th{};
+      if (MODE == LM_DISTILL) {
+        if (ahead_row != r) ahead.load(a, r, 0, lane, 32);
+        th = teacher_head<T>(a, r, tc, ahead, x, g, rg, lane, 32, FULL_MASK);
+        ahead_row = r + pl.units;
+        if (ahead_row < pl.rows) ahead.load(a, ahead_row, 0, lane, 32);
+      }
+
+      Base base;
+      float S;
+      if (PASS1) {
+        wait(&st.red_full[rows_read.i], rows_read.phase);
+        float mb = NEG_INF, s = 0.0f;
+        if (lane < warps) {
+          const float2 v = st.red[rows_read.i][lane];
+          mb = v.x;
+          s = v.y;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st.red_free[rows_read.i]);
+        if (ei >= 0) {
+          const float xv = to_f32<T>(xe), eb = xv * a.sl;
+          join_pair(mb, s, eb, eb == NEG_INF ? 0.0f : ex2(fmaf(xv, a.sl, -eb)));
+        }
+        join_lanes(mb, s);
+        if (pl.cl > 1) {
+          // two barriers and two sets of slots, so that a peer's next row cannot
+          // meet this one's
+          uint64_t* bar = &st.peer[rows_read.i];
+          if (lane == 0) mbar_expect_tx(bar, 8 * pl.cl);
+          __syncwarp();
+          if (lane < pl.cl) {
+            st_async_cluster(&st.part[rows_read.i][pl.rank].x, bar, lane, mb);
+            st_async_cluster(&st.part[rows_read.i][pl.rank].y, bar, lane, s);
+          }
+          if (!wait.dead && !mbar_wait_cluster(bar, rows_read.phase, WAIT_SPIN_LIMIT)) wait.give_up();
+          mb = NEG_INF;
+          s = 0.0f;
+          if (lane < pl.cl) {
+            const float2 v = st.part[rows_read.i][lane];
+            mb = v.x;
+            s = v.y;
+          }
+          join_lanes(mb, s);
+        }
+        rows_read.next();
+        base.at = mb;
+        base.direct = fabsf(mb) <= F32_MAX;
+        S = s;
+        if (!base.direct) {
+          // the scaled scores leave float32 (or the row holds nothing but -inf, or
+          // an infinity): once more over the row, differences first
+          float m = NEG_INF;
+          for (int i = lane; i < a.V; i += 32) m = fmaxf(m, to_f32<T>(x[i]));
+          m = warp_max(m);
+          S = 0.0f;
+          for (int i = lane; i < a.V; i += 32) S += ex2((to_f32<T>(x[i]) - m) * a.sl);
+          S = group_sum(S, 32);
+          base.at = m;
+        }
+      } else {
+        base = unpack_stat(a.stat[r], S);
+      }
+
+      float cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
+      bool zero = false;
+      if (MODE == LM_SCALED) {
+        cy = (float)((double)w * a.s);
+        cq = -cy;
+      } else if (MODE == LM_DISTILL) {
+        P = th.P;
+        zero = th.malformed;
+        cq = (float)((a.w ? a.w[h.b] : 1.0) / a.s);
+      } else {
+        cy = label_outputs<MODE>(a, r, in, base, S, lane == 0 && pl.rank == 0);
+        cq = -cy;
+      }
+      const float scale = cq * P / S;
+      if (GRAD) {
+        note.at = base.at;
+        note.scale = scale;
+        note.cy = cy;
+        note.kind = zero ? NOTE_ZERO : base.direct ? NOTE_DIRECT : NOTE_DIFFERENCE;
+        note.y = has_label(MODE) ? h.y : 0;  // >= 0: the row's chunks are in the ring
+        if (has_label(MODE)) note.gy = based_exp(in.xy(), a.sl, base) * scale + cy;
+        // (published below, before the rest of this row's work)
+        wait(&st.note_free[now.i], now.phase ^ 1);
+        if (lane == 0) {
+          st.note[now.i] = note;
+          mbar_arrive(&st.note_full[now.i]);
+        }
+        if (ei >= 0) {
+          float gv = zero ? 0.0f : based_exp(to_f32<T>(xe), a.sl, base) * scale;
+          if (has_label(MODE) && ei == h.y) gv += cy;
+          if (a.add) gv += to_f32<T>(g[ei]);
+          g[ei] = from_f32<T>(gv);
+        }
+      }
+      if (MODE == LM_DISTILL) {
+        if (zero) {
+          if (lane == 0 && pl.rank == 0) blank_outputs<MODE>(a, r, true);
+        } else {
+          teacher_terms(a, r, tc, th, base, S, pl.rank == 0, lane, 32, FULL_MASK);
+        }
+        __syncwarp();  // the edges are written
+        if (GRAD) {
+          Turn before = now;
+          before.i ^= 1;
+          before.phase ^= (uint32_t)before.i;
+          if (due) settle(before);
+          due = !zero;
+          due_base = base;
+          due_scale = scale;
+          due_cq = cq;
+          due_repeats = th.repeats;
+          due_row = r;
+          due_range = rg;
+        }
+        __syncwarp();
+      }
+    }
+    if (GRAD) {
+      if (blank) {
+        if (MODE == LM_DISTILL && due) {
+          Turn before = now;
+          before.i ^= 1;
+          before.phase ^= (uint32_t)before.i;
+          settle(before);
+        }
+        wait(&st.note_free[now.i], now.phase ^ 1);
+        if (lane == 0) {
+          st.note[now.i] = note;
+          mbar_arrive(&st.note_full[now.i]);
+        }
+      }
+      turn.next();
+    }
+  }
+  if (GRAD && MODE == LM_DISTILL && due) {
+    Turn before = turn;
+    before.i ^= 1;
+    before.phase ^= (uint32_t)before.i;
+    settle(before);
+  }
+}
+
 template <typename T, int MODE, bool GRAD>
 __global__ void __launch_bounds__(RING_THREADS, 1)
     loss_ring_kernel(const __grid_constant__ RowArgs a, const RingShape shape) {
-  constexpr int VE = vec_of<T>;
-  constexpr bool PASS1 = MODE != LM_SCALED;
   extern __shared__ __align__(128) unsigned char ring_smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int W = shape.W, slots = shape.slots, cl = shape.cl, groups = RING_WARPS / W;
-  const int chunk_vecs = W * 32 * RING_NV;
-  const size_t ring_bytes = (size_t)slots * W * RING_WARP_BYTES;
-  RingBars& bars = *reinterpret_cast<RingBars*>(ring_smem + groups * ring_bytes);
-  float* teachers = reinterpret_cast<float*>(&bars + 1);
-  const int rank = cl > 1 ? (int)cluster_ctarank() : 0;
-  const int rows = a.B * a.T, V = a.V;  // rows <= 2^27
-  const int units = (int)(gridDim.x / cl) * groups;
+  constexpr bool PASS1 = MODE != LM_SCALED;
+  constexpr bool BOTH = PASS1 && GRAD;  // half of a group's warps reduce, the others write
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int W = shape.W, groups = RING_WARPS / W;
+  const int role_warps = BOTH ? W / 2 : W;
+  RingPlace pl;
+  pl.cl = shape.cl;
+  pl.slots = shape.slots;
+  pl.chunk_bytes = role_warps * RING_WARP_BYTES;
+  pl.rank = pl.cl > 1 ? (int)cluster_ctarank() : 0;
+  pl.rows = a.B * a.T;  // <= 2^27
+  pl.units = (int)(gridDim.x / pl.cl) * groups;
+  const size_t ring_bytes = (size_t)pl.slots * pl.chunk_bytes;
+  GroupState* states = reinterpret_cast<GroupState*>(ring_smem + groups * ring_bytes);
+  float* teachers = reinterpret_cast<float*>(states + groups);
+  const int first = (int)(blockIdx.x / pl.cl) * groups;
 
-  if (blockIdx.x == 0 && tid == 0 && a.status) *a.status = 0;
-  if (tid == 0) {
-    for (int i = 0; i < groups * slots; ++i) {
-      mbar_init(&bars.full[i], 1);
-      mbar_init(&bars.empty[i], W);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = 0;
+  if (threadIdx.x < groups) {
+    GroupState& st = states[threadIdx.x];
+    for (int i = 0; i < pl.slots; ++i) {
+      mbar_init(&st.full[i], 1);
+      mbar_init(&st.empty[i], role_warps);
     }
-    mbar_init(&bars.peer[0], 1);
-    mbar_init(&bars.peer[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&st.red_full[i], role_warps);
+      mbar_init(&st.red_free[i], 1);
+      mbar_init(&st.note_full[i], 1);
+      mbar_init(&st.note_free[i], role_warps);
+      mbar_init(&st.peer[i], 1);
+    }
     fence_mbar_init();
   }
   __syncthreads();
-  if (cl > 1) cluster_sync();
+  if (pl.cl > 1) cluster_sync();
 
-  if (warp == RING_WARPS) {
-    // ---- the copying warp: lane g feeds group g
-    const bool mine = lane < groups;
-    const int gi = mine ? lane : 0;
-    unsigned char* ring = ring_smem + gi * ring_bytes;
-    uint64_t* full = bars.full + gi * slots;
-    uint64_t* empty = bars.empty + gi * slots;
-    int r = (int)(blockIdx.x / cl) * groups + gi;
-    bool done = !mine || r >= rows, open = false;
-    HeadLoad next{};
-    float next_w = 0.0f;
-    if (!done) {
-      next = load_head<MODE>(a, r);
-      if (MODE == LM_SCALED) next_w = a.wseq[next.b];
-    }
-    Cursor cur{0, 0};
-    const unsigned char* src = nullptr;
-    int left = 0;
-    int idle = 0;
-    while (!__all_sync(FULL_MASK, done)) {
-      bool moved = false;
-      if (!done && !open) {
-        // the head loaded a row ahead; skip rows that are not read
-        if (r >= rows) {
-          done = true;
-        } else {
-          const Head h = make_head<MODE>(a, next);
-          if (!row_blank<MODE>(h, next_w)) {
-            const T* x = row_at<T>(a.x, r, a.ldx);
-            const Part p = part_of(x, V, rank, cl);
-            src = reinterpret_cast<const unsigned char*>(x + p.sp.head) + (size_t)p.lo * 16;
-            left = p.n;
-            open = left > 0;
-          }
-          r += units;
-          if (r < rows) {
-            next = load_head<MODE>(a, r);
-            if (MODE == LM_SCALED) next_w = a.wseq[next.b];
-          }
-        }
-        moved = true;
-      } else if (open && mbar_test(&empty[cur.slot], cur.phase ^ 1)) {
-        const int n = min(left, chunk_vecs);
-        mbar_expect_tx(&full[cur.slot], n * 16);
-        bulk_g2s(ring + (size_t)cur.slot * W * RING_WARP_BYTES, src, n * 16, &full[cur.slot]);
-        src += (size_t)n * 16;
-        left -= n;
-        open = left > 0;
-        cur.next(slots);
-        moved = true;
-      }
-      if (__any_sync(FULL_MASK, moved)) {
-        idle = 0;
-      } else {
-        __nanosleep(64);
-        if (++idle >= WAIT_SPIN_LIMIT) {
-          if (lane == 0 && a.status) set_status(a.status, ST_DEVICE_TIMEOUT);
-          break;
-        }
-      }
-    }
-    // the CTA's shared memory outlives its copies: wait for those still in flight
-    if (mine)
-      for (int i = 0; i < slots; ++i) {
-        // a slot's last copy: of this pass over the ring, or of the one before (a
-        // barrier that was never used counts as past that one)
-        mbar_wait(&full[i], i < cur.slot ? cur.phase : cur.phase ^ 1, WAIT_SPIN_LIMIT);
-      }
+  if (warp == RING_WARPS + groups) {
+    pl.first = first;
+    ring_copier<T, MODE>(a, ring_smem, states, groups, ring_bytes, pl, lane);
     return;
   }
-
-  // ---- consumers
-  const int gi = warp / W, gw = warp - gi * W, gt = gw * 32 + lane, GT = W * 32;
-  const unsigned char* ring = ring_smem + gi * ring_bytes;
-  uint64_t* full = bars.full + gi * slots;
-  uint64_t* empty = bars.empty + gi * slots;
-  float* tm = teachers + (size_t)gi * (MODE == LM_DISTILL ? TEACHER_WORDS * a.k : 0);
-  const Teacher tc{tm, reinterpret_cast<int*>(tm + a.k), tm + 2 * a.k, tm + 3 * a.k};
-  auto group_sync = [&]() {
-    if (W == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + gi), "r"(GT) : "memory");
-  };
-  bool dead = false;  // a wait gave up: wait no more
-  auto gave_up = [&]() {
-    dead = true;
-    if (a.status) set_status(a.status, ST_DEVICE_TIMEOUT);
-  };
-
-  Cursor cur{0, 0};
-  int turn = 0;  // rows joined so far, modulo 2
-  uint32_t peer_phase = 0;
-  int r = (int)(blockIdx.x / cl) * groups + gi;
-  HeadLoad next{};
-  float next_w = 0.0f;
-  if (r < rows) {
-    next = load_head<MODE>(a, r);
-    if (MODE == LM_SCALED) next_w = a.wseq[next.b];
-  }
-  for (; r < rows; r += units) {
-    const Head h = make_head<MODE>(a, next);
-    const float w = next_w;
-    if (r + units < rows) {
-      next = load_head<MODE>(a, r + units);
-      if (MODE == LM_SCALED) next_w = a.wseq[next.b];
-    }
-    const T* x = row_at<T>(a.x, r, a.ldx);
-    T* g = GRAD ? row_at<T>(a.g, r, a.ldg) : nullptr;
-    const Part p = part_of(x, V, rank, cl);
-    const int head = p.sp.head, n = p.n;
-    // gradient rows of another alignment are stored element by element
-    const bool same =
-        GRAD && ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(g)) & 15) == 0;
-    T* gb = GRAD ? g + head + (size_t)p.lo * VE : nullptr;
-    const int ei = rank == 0 && gt < p.sp.edge ? edge_index<T>(p.sp, gt) : -1;
-
-    auto fill_zero = [&]() {
-      if (!GRAD || a.add) return;
-      for (int i = gt; i < n; i += GT) {
-        if (same) {
-          reinterpret_cast<uint4*>(gb)[i] = make_uint4(0, 0, 0, 0);
-        } else {
-          for (int e = 0; e < VE; ++e) gb[(size_t)i * VE + e] = from_f32<T>(0.0f);
-        }
-      }
-      if (ei >= 0) g[ei] = from_f32<T>(0.0f);
-    };
-    if (row_blank<MODE>(h, w)) {
-      if (PASS1 && gt == 0 && rank == 0) blank_outputs<MODE>(a, r, h.live);
-      fill_zero();
-      continue;
-    }
-
-    const int chunks = (n + chunk_vecs - 1) / chunk_vecs;
-    float xe = ei >= 0 ? to_f32<T>(x[ei]) : NEG_INF;
-    const LabelIn in = load_label<T, MODE>(a, r, h, x);
-    const Range rg = rank == 0 ? Range{0, head + n * VE, head + p.sp.nb * VE}
-                               : Range{head + p.lo * VE, head + (p.lo + n) * VE, V};
-    TeacherHead th{};
-    if (MODE == LM_DISTILL && gw == 0) {
-      th = teacher_head<T>(a, r, tc, x, g, rg, lane, 32, FULL_MASK);
-      if (lane == 0) {
-        bars.tshare[turn][gi][0] = th.P;
-        bars.tshare[turn][gi][1] = th.malformed ? 1.0f : 0.0f;
-      }
-    }
-
-    Base base;
-    float S = 0.0f;
-    const Cursor start = cur;
-    if (PASS1) {
-      float mb = xe == NEG_INF ? NEG_INF : xe * a.sl;
-      float s = ei >= 0 ? ex2(mb == NEG_INF ? NEG_INF : fmaf(xe, a.sl, -mb)) : 0.0f;
-      for (int c = 0; c < chunks; ++c) {
-        if (!dead && !mbar_wait(&full[cur.slot], cur.phase, WAIT_SPIN_LIMIT)) gave_up();
-        const uint4* chunk =
-            reinterpret_cast<const uint4*>(ring + (size_t)cur.slot * W * RING_WARP_BYTES);
-        uint4 raw[RING_NV];
-        take_chunk<T>(raw, chunk, gt, GT, n - c * chunk_vecs);
-        if (!GRAD) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[cur.slot]);
-        }
-        const float nb = fmaxf(mb, Vec<T>::greatest(raw) * a.sl);
-        const float at = nb == NEG_INF ? 0.0f : nb;  // nothing above -inf yet: exponentials of 0
-        const f32x2 sl2 = pair(a.sl, a.sl), at2 = pair(-at, -at);
-        f32x2 sum2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
-#pragma unroll
-        for (int i = 0; i < RING_NV; ++i) {
-          f32x2 v[Vec<T>::PAIRS];
-          Vec<T>::unpack(raw[i], v);
-#pragma unroll
-          for (int e = 0; e < Vec<T>::PAIRS; ++e)
-            sum2[e & 1] = add2(sum2[e & 1], ex2_2(fma2(v[e], sl2, at2)));
-        }
-        float sum, odd;
-        halves(add2(sum2[0], sum2[1]), sum, odd);
-        sum += odd;
-        s = (mb == NEG_INF && s == 0.0f ? 0.0f : s * ex2(mb - nb)) + sum;
-        mb = nb;
-        cur.next(slots);
-      }
-      // ---- the row's base and sum
-      join_lanes(mb, s, 32);
-      if (W > 1) {
-        if (lane == 0) bars.red[turn][warp] = make_float2(mb, s);
-        group_sync();
-        const float2 mine = lane < W ? bars.red[turn][gi * W + lane] : make_float2(NEG_INF, 0.0f);
-        mb = mine.x;
-        s = mine.y;
-        join_lanes(mb, s, 32);
-      } else if (MODE == LM_DISTILL) {
-        __syncwarp();
-      }
-      if (cl > 1) {
-        // one group a CTA here (W == RING_WARPS); two barriers and two sets of
-        // slots, so that a peer's next row cannot meet this one's
-        if (gt == 0) mbar_expect_tx(&bars.peer[turn], 8 * cl);
-        if (gt < cl) {
-          st_async_cluster(&bars.part[turn][rank].x, &bars.peer[turn], gt, mb);
-          st_async_cluster(&bars.part[turn][rank].y, &bars.peer[turn], gt, s);
-        }
-        __syncwarp();
-        if (!dead && !mbar_wait_cluster(&bars.peer[turn], peer_phase, WAIT_SPIN_LIMIT)) gave_up();
-        if (turn) peer_phase ^= 1;
-        const float2 mine = lane < cl ? bars.part[turn][lane] : make_float2(NEG_INF, 0.0f);
-        mb = mine.x;
-        s = mine.y;
-        join_lanes(mb, s, 32);
-      }
-      base.at = mb;
-      base.direct = true;
-      S = s;
-      if (!(fabsf(mb) <= F32_MAX)) {
-        // the scaled scores leave float32 (or the row holds nothing but -inf,
-        // or an infinity): once more over the row, differences first
-        float m = NEG_INF;
-        for (int i = gt; i < V; i += GT) m = fmaxf(m, to_f32<T>(x[i]));
-        m = group_max(m, 32);
-        if (W > 1) {
-          group_sync();
-          if (lane == 0) bars.red[turn][warp].x = m;
-          group_sync();
-          m = group_max(lane < W ? bars.red[turn][gi * W + lane].x : NEG_INF, 32);
-        }
-        float t = 0.0f;
-        for (int i = gt; i < V; i += GT) t += ex2((to_f32<T>(x[i]) - m) * a.sl);
-        t = group_sum(t, 32);
-        if (W > 1) {
-          group_sync();
-          if (lane == 0) bars.red[turn][warp].y = t;
-          group_sync();
-          t = group_sum(lane < W ? bars.red[turn][gi * W + lane].y : 0.0f, 32);
-        }
-        base.at = m;
-        base.direct = false;
-        S = t;
-      }
-    }
-
-    float cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
-    bool blank = false;
-    if (MODE == LM_SCALED) {
-      base = unpack_stat(a.stat[r], S);
-      cy = (float)((double)w * a.s);
-      cq = -cy;
-    } else if (MODE == LM_DISTILL) {
-      P = bars.tshare[turn][gi][0];
-      blank = bars.tshare[turn][gi][1] != 0.0f;
-      if (blank) {
-        if (gt == 0 && rank == 0) blank_outputs<MODE>(a, r, true);
-      } else if (gw == 0) {
-        teacher_terms(a, r, tc, th, base, S, rank == 0, lane, 32, FULL_MASK);
-      }
-      cq = (float)((a.w ? a.w[h.b] : 1.0) / a.s);
-      if (GRAD && a.add) group_sync();  // the gradient's old values at the entries are read
+  const int gi = warp < RING_WARPS ? warp / W : warp - RING_WARPS;
+  pl.first = first + gi;
+  pl.ring = ring_smem + gi * ring_bytes;
+  pl.st = states + gi;
+  if (warp >= RING_WARPS) {
+    ring_scalar<T, MODE, GRAD>(a, pl, teachers + (size_t)gi * (MODE == LM_DISTILL ? 2 * TEACHER_WORDS * a.k + teacher_table(a.k) : 0),
+                               role_warps, lane);
+  } else {
+    const int gw = warp - gi * W;
+    if (BOTH) {
+      if (gw < role_warps) ring_reduce<T, MODE, false>(a, pl, gw * 32 + lane, role_warps * 32);
+      else ring_write<T, MODE>(a, pl, (gw - role_warps) * 32 + lane, role_warps * 32);
+    } else if (PASS1) {
+      ring_reduce<T, MODE, true>(a, pl, gw * 32 + lane, role_warps * 32);
     } else {
-      cy = label_outputs<MODE>(a, r, in, base, S, gt == 0 && rank == 0);
-      cq = -cy;
-    }
-    turn ^= 1;
-    if (!GRAD) continue;
-
-    const float scale = cq * P / S;
-    cur = start;
-    for (int c = 0; c < chunks; ++c) {
-      if (!PASS1 && !dead && !mbar_wait(&full[cur.slot], cur.phase, WAIT_SPIN_LIMIT)) gave_up();
-      const uint4* chunk =
-          reinterpret_cast<const uint4*>(ring + (size_t)cur.slot * W * RING_WARP_BYTES);
-      const int have = n - c * chunk_vecs;
-      uint4 raw[RING_NV];
-      take_chunk<T>(raw, chunk, gt, GT, have);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[cur.slot]);
-#pragma unroll
-      for (int i = 0; i < RING_NV; ++i) {
-        if (i * GT + gt >= have) break;
-        const size_t slot = (size_t)c * chunk_vecs + i * GT + gt;
-        f32x2 v[Vec<T>::PAIRS];
-        Vec<T>::unpack(raw[i], v);
-        if (base.direct) {
-          const f32x2 sl2 = pair(a.sl, a.sl), at2 = pair(-base.at, -base.at),
-                      scale2 = pair(scale, scale);
-#pragma unroll
-          for (int e = 0; e < Vec<T>::PAIRS; ++e) v[e] = mul2(ex2_2(fma2(v[e], sl2, at2)), scale2);
-        } else {
-#pragma unroll
-          for (int e = 0; e < Vec<T>::PAIRS; ++e) {
-            float lo, hi;
-            halves(v[e], lo, hi);
-            v[e] = pair(based_exp(lo, a.sl, base) * scale, based_exp(hi, a.sl, base) * scale);
-          }
-        }
-        if (MODE == LM_DISTILL && blank) {
-#pragma unroll
-          for (int e = 0; e < Vec<T>::PAIRS; ++e) v[e] = pair(0.0f, 0.0f);
-        }
-        if (sizeof(T) == 4 && a.add) {
-#pragma unroll
-          for (int e = 0; e < Vec<T>::PAIRS; ++e)
-            v[e] = add2(v[e], pair(to_f32<T>(gb[slot * VE + 2 * e]), to_f32<T>(gb[slot * VE + 2 * e + 1])));
-        }
-        const uint4 q = Vec<T>::pack(v);
-        if (same) {
-          reinterpret_cast<uint4*>(gb)[slot] = q;
-        } else {
-          const T* each = reinterpret_cast<const T*>(&q);
-#pragma unroll
-          for (int e = 0; e < VE; ++e) gb[slot * VE + e] = each[e];
-        }
-      }
-      cur.next(slots);
-    }
-    if (ei >= 0) {
-      float gv = blank ? 0.0f : based_exp(xe, a.sl, base) * scale;
-      if (a.add) gv += to_f32<T>(g[ei]);
-      g[ei] = from_f32<T>(gv);
-    }
-    if (has_label(MODE)) {
-      // the thread that wrote the label's element puts it right
-      const int at = h.y - head - p.lo * VE;
-      const bool owner = at >= 0 && at < n * VE ? at / VE % GT == gt : ei == h.y;
-      if (owner) {
-        float gv = based_exp(in.xy, a.sl, base) * scale + cy;
-        if (a.add) gv = to_f32<T>(g[h.y]) + cy;
-        g[h.y] = from_f32<T>(gv);
-      }
-    } else {
-      group_sync();  // this CTA's part of the row is written; its teacher entries follow
-      if (gw == 0 && !blank) teacher_fix<T>(a, tc, g, base, scale, cq, lane, 32, rg);
-      __syncwarp();
+      ring_write<T, MODE>(a, pl, gw * 32 + lane, role_warps * 32);
     }
   }
 }
 
-// Warps a group: enough rows in flight to hide one row's join behind the
-// others', without cutting the rings below a row and a half.
+// Warps a group.
 inline int ring_warps(size_t row_bytes) {
-  int W = 1;
+  int W = 2;
   while (W < RING_WARPS && row_bytes > (size_t)W * 8 * 1024) W *= 2;
   return W;
 }
@@ -489,27 +683,27 @@ inline int ring_warps(size_t row_bytes) {
 // False where a row with a gradient does not fit the rings of a cluster.
 template <typename T, int MODE>
 bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
-  const bool grad = a.g != nullptr;
-  const bool hold = grad && MODE != LM_SCALED && MODE != LM_PREFERENCE;  // the row stays in the ring between the passes
+  const bool grad = a.g != nullptr && MODE != LM_PREFERENCE;
+  const bool hold = grad && MODE != LM_SCALED;  // the row stays in the ring between the passes
   const size_t row = (size_t)a.V * sizeof(T);
-  const size_t entry = MODE == LM_DISTILL ? (size_t)TEACHER_WORDS * a.k * sizeof(float) : 0;
+  const size_t entry = MODE == LM_DISTILL ? (2ull * TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float) : 0;
   RingShape s;
   s.W = ring_warps(row);
-  while (s.W < RING_WARPS && RING_WARPS / s.W * entry > 24 * 1024) s.W *= 2;
-  size_t room, chunk;
+  while (s.W < RING_WARPS && RING_WARPS / s.W * entry > 40 * 1024) s.W *= 2;
+  size_t chunk, fixed;
   for (;; s.W *= 2) {
     const int groups = RING_WARPS / s.W;
-    chunk = (size_t)s.W * RING_WARP_BYTES;
-    room = (RING_SMEM - sizeof(RingBars) - groups * entry) / groups;
-    s.slots = (int)std::min<size_t>(RING_SLOTS_MAX, room / chunk);
+    chunk = (size_t)(hold ? s.W / 2 : s.W) * RING_WARP_BYTES;
+    fixed = groups * (sizeof(GroupState) + entry);
+    s.slots = (int)std::min<size_t>(RING_SLOTS_MAX, (RING_SMEM - fixed) / groups / chunk);
     if (!hold || row <= (size_t)(s.slots - 1) * chunk || s.W == RING_WARPS) break;
   }
   s.cl = 1;
-  if (hold && row > (size_t)(s.slots - 1) * chunk)
-    while (s.cl <= RING_CLUSTER_MAX && row > (size_t)s.cl * (s.slots - 1) * chunk) s.cl *= 2;
+  if (hold)
+    while (s.cl <= RING_CLUSTER_MAX && row > (size_t)s.cl * (s.slots - 1) * chunk) ++s.cl;
   if (s.cl > RING_CLUSTER_MAX) return false;
   const int groups = RING_WARPS / s.W;
-  const size_t smem = groups * (s.slots * chunk + entry) + sizeof(RingBars);
+  const size_t smem = groups * s.slots * chunk + fixed;
   void (*kern)(const RowArgs, const RingShape) =
       grad ? (void (*)(const RowArgs, const RingShape))loss_ring_kernel<T, MODE, MODE != LM_PREFERENCE>
            : (void (*)(const RowArgs, const RingShape))loss_ring_kernel<T, MODE, MODE == LM_SCALED>;
@@ -519,7 +713,7 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   const long long rows = (long long)a.B * a.T;
   const long long want = (rows + groups - 1) / groups * s.cl;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(RING_THREADS);
+  cfg.blockDim = dim3((RING_WARPS + groups + 1) * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -528,8 +722,17 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = s.cl > 1 ? 1 : 0;
-  const int sms = loss_sm_count();
-  cfg.gridDim = dim3((unsigned)std::min<long long>(want, sms / s.cl * s.cl));
+  // one CTA an SM; clusters only as many as run at once (a GPC need not hold a
+  // multiple of cl SMs, and a second wave would take as long as the first)
+  int fit = loss_sm_count();
+  if (s.cl > 1) {
+    cfg.gridDim = dim3((unsigned)(fit / s.cl * s.cl));
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+    if (e != cudaSuccess) return true;
+    fit = std::max(1, clusters) * s.cl;
+  }
+  cfg.gridDim = dim3((unsigned)std::min<long long>(want, fit));
   e = cudaLaunchKernelEx(&cfg, kern, a, s);
   return true;
 }

@@ -24,6 +24,10 @@
 
 #include "loss.cuh"
 
+#ifndef LOSS_POLY
+#define LOSS_POLY 9
+#endif
+
 namespace semicrf {
 
 namespace {
@@ -75,8 +79,8 @@ __device__ __forceinline__ float based_exp(float x, float sl, const Base& h) {
 
 // The base in the scores' units.  sl is rounded to float32; taking the base
 // over that same factor keeps its error out of the dominant terms of the sum.
-__device__ __forceinline__ double base_score(const Base& h, float sl) {
-  return h.direct ? (double)h.at / (double)sl : (double)h.at;
+__device__ __forceinline__ double base_score(const Base& h, double inv_sl) {
+  return h.direct ? (double)h.at * inv_sl : (double)h.at;
 }
 
 // (base, sum) of a row in one float2: a sum is positive, so its sign tells which base it is.
@@ -142,19 +146,21 @@ __device__ __forceinline__ Head make_head(const RowArgs& a, const HeadLoad& l) {
 }
 
 // The per-position inputs of a label loss, loaded when its row starts.
+template <typename T>
 struct LabelIn {
-  float xy;  // score of the label
+  T score;  // of the label, as loaded: converting it would wait for it
   float slope, old_logp, ref_logp, adv;
   double w;
+  __device__ float xy() const { return to_f32<T>(score); }
 };
 
 template <typename T, int MODE>
-__device__ __forceinline__ LabelIn load_label(const RowArgs& a, long long r, const Head& h,
+__device__ __forceinline__ LabelIn<T> load_label(const RowArgs& a, long long r, const Head& h,
                                               const T* x) {
-  LabelIn in{};
+  LabelIn<T> in{};
   in.w = 1.0;
   if (!has_label(MODE)) return in;
-  in.xy = to_f32<T>(x[h.y]);
+  in.score = x[h.y];
   if (MODE == LM_LOGPROB) in.slope = a.grad_logp ? a.grad_logp[r] : 1.0f;
   if (MODE == LM_PREFERENCE || MODE == LM_POLICY) in.ref_logp = a.ref_logp ? a.ref_logp[r] : 0.0f;
   if (MODE == LM_POLICY) {
@@ -179,10 +185,10 @@ __device__ __forceinline__ void blank_outputs(const RowArgs& a, long long r, boo
 
 // What follows from a row's base and sum for a label loss: the position's
 // outputs (written by one thread) and d loss / d logp / temperature.
-template <int MODE>
-__device__ __forceinline__ float label_outputs(const RowArgs& a, long long r, const LabelIn& in,
+template <int MODE, typename T>
+__device__ __forceinline__ float label_outputs(const RowArgs& a, long long r, const LabelIn<T>& in,
                                                const Base& h, float S, bool writer) {
-  const double logp = ((double)in.xy - base_score(h, a.sl)) * a.s - log_of_sum(S);
+  const double logp = ((double)in.xy() - base_score(h, a.inv_sl)) * a.s - log_of_sum(S);
   float slope = in.slope;
   float term = (float)logp;
   if (MODE == LM_PREFERENCE) term = (float)(logp - (double)in.ref_logp);
@@ -213,13 +219,25 @@ struct Teacher {
   int* id;     // [k]
   float* x;    // [k] the row's scores at those labels
   float* old;  // [k] the gradient's value before this call (accumulation)
+  int* table;  // [teacher_table(k)] scratch
 };
 
 constexpr int TEACHER_WORDS = 4;
 
+// Size of the hash table that tells whether a label comes twice: none for
+// short lists, whose entries are compared with one another.
+constexpr int TEACHER_SHORT = 16;
+__host__ __device__ inline int teacher_table(int k) {
+  if (k <= TEACHER_SHORT) return 0;
+  int n = 64;
+  while (n < 2 * k) n *= 2;
+  return n;
+}
+
 struct TeacherHead {
   float tm, tlog, P;
   bool malformed;
+  bool repeats;  // two entries may have the same label
 };
 
 // The elements of a row that a CTA writes: [lo, hi) and those from `tail` on.
@@ -238,25 +256,52 @@ __device__ __forceinline__ float lanes_sum(float v, int n, unsigned mm) {
   return v;
 }
 
-// Loads the entries; the maximum and log-sum-exp of the teacher's logits over
-// those in use.
+// The first TEACHER_AHEAD entries of each lane, loaded before they are needed.
+constexpr int TEACHER_AHEAD = 4;
+struct TeacherAhead {
+  int id[TEACHER_AHEAD];
+  float t[TEACHER_AHEAD];
+  __device__ __forceinline__ void load(const RowArgs& a, long long r, int from, int lane, int n) {
+#pragma unroll
+    for (int u = 0; u < TEACHER_AHEAD; ++u) {
+      const int j = from + u * n + lane;
+      id[u] = j < a.k ? a.ids[r * a.k + j] : -1;
+      t[u] = j < a.k ? a.tl[r * a.k + j] : NEG_INF;
+    }
+  }
+};
+
+// Takes the entries in (the first ones are in `ahead`); the maximum and
+// log-sum-exp of the teacher's logits over those in use.
 template <typename T>
 __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long r, const Teacher& tc,
-                                                    const T* x, const T* g, const Range& rg,
-                                                    int lane, int n, unsigned mm) {
+                                                    TeacherAhead& ahead, const T* x, const T* g,
+                                                    const Range& rg, int lane, int n, unsigned mm) {
   TeacherHead th;
   const float st = (float)a.s;
   float out = 0.0f, m = NEG_INF;
-  for (int j = lane; j < a.k; j += n) {
-    const int id = a.ids[r * a.k + j];
-    const bool inside = id >= 0 && id < a.V;
-    const float t = inside ? a.tl[r * a.k + j] : NEG_INF;
-    if (id >= a.V) out = 1.0f;
-    tc.id[j] = inside ? id : -1;
-    tc.p[j] = t;
-    tc.x[j] = inside ? to_f32<T>(x[id]) : 0.0f;
-    if (a.add && g && inside && rg.has(id)) tc.old[j] = to_f32<T>(g[id]);
-    m = fmaxf(m, t);
+  for (int from = 0; from < a.k; from += TEACHER_AHEAD * n) {
+    if (from) ahead.load(a, r, from, lane, n);
+    T xs[TEACHER_AHEAD];
+#pragma unroll
+    for (int u = 0; u < TEACHER_AHEAD; ++u) {
+      const bool inside = ahead.id[u] >= 0 && ahead.id[u] < a.V;
+      xs[u] = from_f32<T>(0.0f);
+      if (inside) xs[u] = x[ahead.id[u]];
+      if (ahead.id[u] >= a.V) out = 1.0f;
+      if (!inside) ahead.id[u] = -1;
+    }
+#pragma unroll
+    for (int u = 0; u < TEACHER_AHEAD; ++u) {
+      const int j = from + u * n + lane, id = ahead.id[u];
+      if (j >= a.k) break;
+      const float t = id >= 0 ? ahead.t[u] : NEG_INF;
+      tc.id[j] = id;
+      tc.p[j] = t;
+      tc.x[j] = to_f32<T>(xs[u]);
+      if (a.add && g && id >= 0 && rg.has(id)) tc.old[j] = to_f32<T>(g[id]);
+      m = fmaxf(m, t);
+    }
   }
   th.malformed = lanes_max(out, n, mm) > 0.0f;
   m = lanes_max(m, n, mm);
@@ -272,6 +317,24 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
     th.tlog = logf(s);
     th.P = s > 0.0f ? 1.0f : s;  // no entry with a probability: no loss, no gradient
   }
+  th.repeats = true;
+  const int size = teacher_table(a.k);
+  if (size) {
+    // open addressing; the table is at least half empty, so that every probe ends
+    for (int i = lane; i < size; i += n) tc.table[i] = -1;
+    __syncwarp(mm);
+    float twice = 0.0f;
+    for (int j = lane; j < a.k; j += n) {
+      const int id = tc.id[j];
+      if (id < 0) continue;
+      for (unsigned at = (unsigned)id * 2654435769u;; ++at) {
+        const int was = atomicCAS(&tc.table[at & (size - 1)], -1, id);
+        if (was == id) twice = 1.0f;
+        if (was == -1 || was == id) break;
+      }
+    }
+    th.repeats = lanes_max(twice, n, mm) > 0.0f;
+  }
   return th;
 }
 
@@ -279,7 +342,7 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
 __device__ __forceinline__ void teacher_terms(const RowArgs& a, long long r, const Teacher& tc,
                                               const TeacherHead& th, const Base& h, float S,
                                               bool loss, int lane, int n, unsigned mm) {
-  const double logS = log_of_sum(S), m = base_score(h, a.sl);
+  const double logS = log_of_sum(S), m = base_score(h, a.inv_sl);
   float part = 0.0f;
   for (int j = lane; j < a.k; j += n) {
     float p = 0.0f;
@@ -303,19 +366,22 @@ __device__ __forceinline__ void teacher_terms(const RowArgs& a, long long r, con
 // over them, in order).
 template <typename T>
 __device__ __forceinline__ void teacher_fix(const RowArgs& a, const Teacher& tc, T* g,
-                                            const Base& h, float scale, float cq, int lane, int n,
-                                            const Range& rg) {
+                                            const Base& h, float scale, float cq, bool repeats,
+                                            int lane, int n, const Range& rg) {
   for (int j = lane; j < a.k; j += n) {
     const int id = tc.id[j];
     if (id < 0 || !rg.has(id)) continue;
-    bool first = true;
-    float p = 0.0f;
-    for (int i = 0; i < a.k; ++i) {
-      if (tc.id[i] != id) continue;
-      if (i < j) first = false;
-      p += tc.p[i];
+    float p = tc.p[j];
+    if (repeats) {
+      bool first = true;
+      p = 0.0f;
+      for (int i = 0; i < a.k; ++i) {
+        if (tc.id[i] != id) continue;
+        if (i < j) first = false;
+        p += tc.p[i];
+      }
+      if (!first) continue;
     }
-    if (!first) continue;
     float gv = based_exp(tc.x[j], a.sl, h) * scale - cq * p;
     if (a.add) gv += tc.old[j];
     g[id] = from_f32<T>(gv);
@@ -356,6 +422,40 @@ __device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
   float lo, hi;
   halves(v, lo, hi);
   return pair(ex2(lo), ex2(hi));
+}
+
+// 2^t for t <= 0 on the FMA pipe, beside the special-function unit's ex2 (16 a
+// clock and SM): t is split into its nearest integer n and f in [-1/2, 1/2]
+// (Cody and Waite), 2^f is the degree-5 polynomial of least relative error
+// there (Remez exchange; 2e-7 with its coefficients and steps in float32, as
+// ex2.approx), and 2^n is put together from its exponent.  Below -127 the
+// result is 0 exactly; a NaN stays one.
+__device__ __forceinline__ f32x2 ex2_2_poly(f32x2 t) {
+  float lo, hi;
+  halves(t, lo, hi);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(-127.0f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(-127.0f));
+  t = pair(lo, hi);
+  constexpr float round = 12582912.0f;  // 1.5 * 2^23: adding it leaves the nearest integer
+  const f32x2 n = add2(t, pair(round, round));
+  const f32x2 f = add2(t, mul2(add2(n, pair(-round, -round)), pair(-1.0f, -1.0f)));
+  f32x2 p = pair(0.0013276472f, 0.0013276472f);
+  p = fma2(p, f, pair(0.009675541f, 0.009675541f));
+  p = fma2(p, f, pair(0.05550713f, 0.05550713f));
+  p = fma2(p, f, pair(0.2402212f, 0.2402212f));
+  p = fma2(p, f, pair(0.69314694f, 0.69314694f));
+  p = fma2(p, f, pair(1.0000001f, 1.0000001f));
+  halves(n, lo, hi);
+  const float el = __int_as_float((__float_as_int(lo) << 23) + 0x3f800000);
+  const float eh = __int_as_float((__float_as_int(hi) << 23) + 0x3f800000);
+  return mul2(p, pair(el, eh));
+}
+
+// Exponentials of pair e of a vector: of the 16-bit types, whose elements are
+// cheap to move, every fourth pair takes the FMA pipe.
+template <typename T>
+__device__ __forceinline__ f32x2 ex2_of_pair(f32x2 v, int e) {
+  return sizeof(T) == 2 && e == LOSS_POLY ? ex2_2_poly(v) : ex2_2(v);
 }
 
 // A 16-byte vector of T as pairs of float32, its greatest element, -inf, and back.

@@ -38,11 +38,14 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
   bool blank = !h.live || h.malformed || (MODE == LM_SCALED && w == 0.0f);
   bool malformed = h.live;
   const Range all{0, V, V};
-  Teacher tc{dyn, reinterpret_cast<int*>(dyn + a.k), dyn + 2 * a.k, dyn + 3 * a.k};
+  Teacher tc{dyn, reinterpret_cast<int*>(dyn + a.k), dyn + 2 * a.k, dyn + 3 * a.k,
+             reinterpret_cast<int*>(dyn + TEACHER_WORDS * a.k)};
   TeacherHead th{};
   if (MODE == LM_DISTILL && h.live) {
     if (warp == 0) {
-      th = teacher_head<T>(a, r, tc, x, g, all, lane, 32, FULL_MASK);
+      TeacherAhead ahead;
+      ahead.load(a, r, 0, lane, 32);
+      th = teacher_head<T>(a, r, tc, ahead, x, g, all, lane, 32, FULL_MASK);
       if (lane == 0) {
         tshare[0] = th.P;
         tshare[1] = th.malformed ? 1.0f : 0.0f;
@@ -100,13 +103,13 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
   }
   if (MODE == LM_DISTILL) {
     __syncthreads();  // the row is written; its teacher entries follow
-    if (warp == 0) teacher_fix<T>(a, tc, g, base, scale, cq, lane, 32, all);
+    if (warp == 0) teacher_fix<T>(a, tc, g, base, scale, cq, th.repeats, lane, 32, all);
   }
 }
 
 template <typename T, int MODE>
 cudaError_t launch_wide(const RowArgs& a, cudaStream_t st) {
-  const size_t smem = MODE == LM_DISTILL ? (size_t)TEACHER_WORDS * a.k * sizeof(float) : 0;
+  const size_t smem = MODE == LM_DISTILL ? (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float) : 0;
   loss_wide_kernel<T, MODE><<<(unsigned)((long long)a.B * a.T), WIDE_THREADS, smem, st>>>(a);
   return cudaGetLastError();
 }
