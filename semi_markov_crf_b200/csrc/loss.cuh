@@ -94,6 +94,18 @@ inline cudaError_t launch_loss_rows(int mode, int type, const RowArgs& a, cudaSt
                         : type == LT_BF16 ? launch_rows_bf16(mode, a, st) : launch_rows_f16(mode, a, st);
 }
 int loss_sm_count();  // of the current device
+
+// A launch that may be set up while the kernel before it in the stream ends:
+// the kernel calls after_previous() before it touches anything.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+inline cudaLaunchAttribute follows() {
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  return at;
+}
 cudaError_t launch_loss_sums(const SeqArgs& a, cudaStream_t st);
 cudaError_t launch_loss_pairs(const SeqArgs& a, cudaStream_t st);
 

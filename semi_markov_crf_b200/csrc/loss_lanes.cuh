@@ -2,105 +2,207 @@
 // NE elements each (included by loss_row.cuh).
 //
 // Rows of a few hundred bytes come by the hundred thousand (the emissions of
-// a batch of sequences), so what counts is instructions a row: the groups of a
-// warp work on neighbouring rows, the loads of a warp are one contiguous
-// stretch of memory, and reductions are log2 L shuffles.
+// a batch of sequences).  What counts is instructions a row (the scalar work
+// of a position costs as much as its elements) and latency: few lanes a row,
+// so that a warp works on several, reductions of log2 L shuffles, and
+// persistent groups that load the next row and the head after that while they
+// work on this one.  VEC: 16-byte loads and stores (rows on 16-byte
+// boundaries); otherwise element by element, neighbouring lanes neighbouring
+// elements.
 
 constexpr int LANES_THREADS = 128;
+constexpr int LANES_CTAS = 7;  // an SM, by registers
+constexpr int LANES_V_MAX = 512;
 
-template <typename T, int MODE, int L, int NE>
-__global__ void __launch_bounds__(LANES_THREADS) loss_lanes_kernel(
-    const __grid_constant__ RowArgs a) {
-  extern __shared__ float dyn[];
-  const int tid = threadIdx.x, V = a.V;
-  const long long r = (long long)blockIdx.x * (blockDim.x / L) + tid / L;
-  if (blockIdx.x == 0 && tid == 0 && a.status) *a.status = 0;
-  if (r >= (long long)a.B * a.T) return;
-  const int lane = tid % L;
-  const unsigned mm = L == 32 ? FULL_MASK : ((1u << (L & 31)) - 1u) << ((tid & 31) / L * L);
-  const Head h = make_head<MODE>(a, load_head<MODE>(a, r));
-  const T* x = row_at<T>(a.x, r, a.ldx);
-  T* g = a.g ? row_at<T>(a.g, r, a.ldg) : nullptr;
-  const float w = MODE == LM_SCALED && h.live ? a.wseq[h.b] : 0.0f;
-  if (!h.live || h.malformed || (MODE == LM_SCALED && w == 0.0f)) {
-    if (MODE != LM_SCALED && lane == 0) blank_outputs<MODE>(a, r, h.live);
-    if (g && !a.add)
-      for (int v = lane; v < V; v += L) g[v] = from_f32<T>(0.0f);
-    return;
+// A row as loaded.
+template <typename T, int NE, bool VEC>
+struct LaneRow {
+  uint4 q[VEC ? NE / vec_of<T> : 1];
+  T e[VEC ? 1 : NE];
+};
+
+template <typename T, int L, int NE, bool VEC>
+struct LaneMap {
+  static constexpr int VE = VEC ? vec_of<T> : 1;
+  // element of this lane's i-th
+  static __device__ __forceinline__ int at(int i, int lane) {
+    return (i / VE) * (L * VE) + lane * VE + i % VE;
   }
+};
 
-  TeacherAhead ahead;
-  if (MODE == LM_DISTILL) ahead.load(a, r, 0, lane, L);
-  float v[NE];
-#pragma unroll
-  for (int i = 0; i < NE; ++i) v[i] = i * L + lane < V ? to_f32<T>(x[i * L + lane]) : NEG_INF;
-  const LabelIn<T> in = load_label<T, MODE>(a, r, h, x);
+template <typename T, int MODE, int L, int NE, bool VEC>
+__global__ void __launch_bounds__(LANES_THREADS, LANES_CTAS)
+    loss_lanes_kernel(const __grid_constant__ RowArgs a) {
+  using Map = LaneMap<T, L, NE, VEC>;
+  constexpr int VE = vec_of<T>;
+  extern __shared__ float dyn[];
+  const int tid = threadIdx.x, V = a.V, lane = tid % L;
+  const int rows = a.B * a.T;  // <= 2^27
+  const int units = (int)(gridDim.x * (blockDim.x / L));
+  int r = (int)(blockIdx.x * (blockDim.x / L) + tid / L);
+  if (blockIdx.x == 0 && tid == 0 && a.status) *a.status = 0;
+  if (r >= rows) return;
+  const unsigned mm = L == 32 ? FULL_MASK : ((1u << (L & 31)) - 1u) << ((tid & 31) / L * L);
   const Range all{0, V, V};
   float* mine =
       dyn + (size_t)(tid / L) * (MODE == LM_DISTILL ? TEACHER_WORDS * a.k + teacher_table(a.k) : 0);
-  Teacher tc{mine, reinterpret_cast<int*>(mine + a.k), mine + 2 * a.k, mine + 3 * a.k,
-             reinterpret_cast<int*>(mine + TEACHER_WORDS * a.k)};
-  TeacherHead th{};
-  if (MODE == LM_DISTILL) {
-    th = teacher_head<T>(a, r, tc, ahead, x, g, all, lane, L, mm);
-    if (th.malformed) {
-      if (lane == 0) blank_outputs<MODE>(a, r, true);
-      if (g && !a.add)
-        for (int i = lane; i < V; i += L) g[i] = from_f32<T>(0.0f);
-      return;
+  const Teacher tc{mine, reinterpret_cast<int*>(mine + a.k), mine + 2 * a.k, mine + 3 * a.k,
+                   reinterpret_cast<int*>(mine + TEACHER_WORDS * a.k)};
+
+  // the row at hand and what is on its way for it
+  struct Load {
+    Head h;
+    bool blank;
+    float w;
+    float2 stat;
+    LabelIn<T> in;
+    LaneRow<T, NE, VEC> x;
+    TeacherAhead ahead;
+  };
+  auto start = [&](Load& l, const HeadLoad& head, int row) {
+    l.h = make_head<MODE>(a, head);
+    l.w = MODE == LM_SCALED && l.h.live ? a.wseq[l.h.b] : 0.0f;
+    l.blank = !l.h.live || l.h.malformed;
+    if (l.blank) return;
+    const T* x = row_at<T>(a.x, row, a.ldx);
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < NE / VE; ++i)
+        if (Map::at(i * VE, lane) < V)
+          l.x.q[i] = __ldg(reinterpret_cast<const uint4*>(x) + (i * L + lane));
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (Map::at(i, lane) < V) l.x.e[i] = x[Map::at(i, lane)];
     }
-  }
+    if (MODE == LM_SCALED) l.stat = a.stat[row];
+    if (has_label(MODE) && MODE != LM_SCALED) l.in = load_label<T, MODE>(a, row, l.h, x);
+    if (MODE == LM_DISTILL) l.ahead.load(a, row, 0, lane, L);
+  };
 
-  Base base;
-  float S;
-  if (MODE == LM_SCALED) {
-    base = unpack_stat(a.stat[r], S);
-  } else {
-    float m = NEG_INF;
+  Load now;
+  start(now, load_head<MODE>(a, r), r);
+  HeadLoad soon{};
+  if (r + units < rows) soon = load_head<MODE>(a, r + units);
+  for (; r < rows; r += units) {
+    Load next;
+    next.blank = true;
+    if (r + units < rows) {
+      start(next, soon, r + units);
+      if (r + 2 * (long long)units < rows) soon = load_head<MODE>(a, r + 2 * units);
+    }
+    const T* x = row_at<T>(a.x, r, a.ldx);
+    T* g = a.g && MODE != LM_PREFERENCE ? row_at<T>(a.g, r, a.ldg) : nullptr;
+    bool blank = now.blank || (MODE == LM_SCALED && now.w == 0.0f);
+    bool malformed = now.blank && now.h.live;
+    TeacherHead th{};
+    if (MODE == LM_DISTILL && !blank) {
+      th = teacher_head<T>(a, r, tc, now.ahead, x, g, all, lane, L, mm);
+      blank = malformed = th.malformed;
+    }
+    if (blank) {
+      if (MODE != LM_SCALED && lane == 0) blank_outputs<MODE>(a, r, malformed);
+      if (g && !a.add)
+        for (int v = lane; v < V; v += L) g[v] = from_f32<T>(0.0f);
+      now = next;
+      continue;
+    }
+
+    float v[NE];
+    if (VEC) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) m = fmaxf(m, v[i]);
-    m = lanes_max(m, L, mm);
-    base = make_base(m, a.sl);
-    S = 0.0f;
-  }
+      for (int i = 0; i < NE / VE; ++i) {
+        f32x2 two[Vec<T>::PAIRS];
+        Vec<T>::unpack(now.x.q[i], two);
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
+        for (int e = 0; e < Vec<T>::PAIRS; ++e) halves(two[e], v[i * VE + 2 * e], v[i * VE + 2 * e + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = to_f32<T>(now.x.e[i]);
+    }
+
+    Base base;
+    float S = 0.0f;
+    if (MODE == LM_SCALED) {
+      base = unpack_stat(now.stat, S);
+    } else {
+      float m = NEG_INF;
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (Map::at(i, lane) < V) m = fmaxf(m, v[i]);
+      base = make_base(lanes_max(m, L, mm), a.sl);
+    }
     // past the row: no score, whatever the base is (-inf - -inf is not a number)
-    v[i] = i * L + lane < V ? based_exp(v[i], a.sl, base) : 0.0f;
-    if (MODE != LM_SCALED) S += v[i];
-  }
-  if (MODE != LM_SCALED) S = lanes_sum(S, L, mm);
-
-  float cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
-  if (MODE == LM_SCALED) {
-    cy = (float)((double)w * a.s);
-    cq = -cy;
-  } else if (MODE == LM_DISTILL) {
-    P = th.P;
-    teacher_terms(a, r, tc, th, base, S, true, lane, L, mm);
-    cq = (float)((a.w ? a.w[h.b] : 1.0) / a.s);
-  } else {
-    cy = label_outputs<MODE>(a, r, in, base, S, lane == 0);
-    cq = -cy;
-  }
-  if (!g || MODE == LM_PREFERENCE) return;
-  const float scale = cq * P / S;
+    if (base.direct) {
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = i * L + lane;
-    if (e >= V) continue;
-    float gv = v[i] * scale;
-    if (has_label(MODE) && e == h.y) gv += cy;
-    if (a.add) gv += to_f32<T>(g[e]);
-    g[e] = from_f32<T>(gv);
-  }
-  if (MODE == LM_DISTILL) {
-    __syncwarp(mm);  // the row is written; its teacher entries follow
-    teacher_fix<T>(a, tc, g, base, scale, cq, th.repeats, lane, L, all);
+      for (int i = 0; i < NE; ++i) v[i] = Map::at(i, lane) < V ? ex2(fmaf(v[i], a.sl, -base.at)) : 0.0f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = Map::at(i, lane) < V ? ex2((v[i] - base.at) * a.sl) : 0.0f;
+    }
+    if (MODE != LM_SCALED) {
+      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < NE; ++i) part[i & 3] += v[i];
+      S = lanes_sum((part[0] + part[1]) + (part[2] + part[3]), L, mm);
+    }
+
+    float cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
+    if (MODE == LM_SCALED) {
+      cy = (float)((double)now.w * a.s);
+      cq = -cy;
+    } else if (MODE == LM_DISTILL) {
+      P = th.P;
+      teacher_terms(a, r, tc, th, base, S, true, lane, L, mm);
+      cq = (float)((a.w ? a.w[now.h.b] : 1.0) / a.s);
+    } else {
+      cy = label_outputs<MODE>(a, r, now.in, base, S, lane == 0);
+      cq = -cy;
+    }
+    if (g) {
+      const float scale = cq * P / S;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        v[i] *= scale;
+        if (has_label(MODE) && Map::at(i, lane) == now.h.y) v[i] += cy;
+      }
+      if (VEC) {
+        uint4* out = reinterpret_cast<uint4*>(g);
+#pragma unroll
+        for (int i = 0; i < NE / VE; ++i) {
+          if (Map::at(i * VE, lane) >= V) continue;
+          f32x2 two[Vec<T>::PAIRS];
+#pragma unroll
+          for (int e = 0; e < Vec<T>::PAIRS; ++e) two[e] = pair(v[i * VE + 2 * e], v[i * VE + 2 * e + 1]);
+          if (sizeof(T) == 4 && a.add) {
+            f32x2 old[Vec<T>::PAIRS];
+            Vec<T>::unpack(out[i * L + lane], old);
+#pragma unroll
+            for (int e = 0; e < Vec<T>::PAIRS; ++e) two[e] = add2(two[e], old[e]);
+          }
+          out[i * L + lane] = Vec<T>::pack(two);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+          const int e = Map::at(i, lane);
+          if (e >= V) continue;
+          if (a.add) v[i] += to_f32<T>(g[e]);
+          g[e] = from_f32<T>(v[i]);
+        }
+      }
+      if (MODE == LM_DISTILL) {
+        __syncwarp(mm);  // the row is written; its teacher entries follow
+        teacher_fix<T>(a, tc, g, base, scale, cq, th.repeats, lane, L, all);
+      }
+    }
+    if (MODE == LM_DISTILL) __syncwarp(mm);
+    now = next;
   }
 }
 
-template <typename T, int MODE, int L, int NE>
+template <typename T, int MODE, int L, int NE, bool VEC>
 cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
   // 48 KB of shared memory for the teacher's entries: fewer rows a CTA where k is large
   int threads = LANES_THREADS;
@@ -111,28 +213,43 @@ cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
     smem = threads / L * row;
   }
   const long long rows = (long long)a.B * a.T, per = threads / L;
-  loss_lanes_kernel<T, MODE, L, NE>
-      <<<(unsigned)((rows + per - 1) / per), threads, smem, st>>>(a);
+  const long long fit = (long long)loss_sm_count() * LANES_CTAS * (LANES_THREADS / threads);
+  loss_lanes_kernel<T, MODE, L, NE, VEC>
+      <<<(unsigned)std::min(fit, (rows + per - 1) / per), threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
-// False where the row is too long for these kernels (or the teacher's lists
-// do not fit 48 KB for one warp's rows).
+template <typename T, int MODE, int L>
+cudaError_t launch_lanes_of(const RowArgs& a, cudaStream_t st) {
+  constexpr int VE = vec_of<T>;
+  const bool grad = a.g != nullptr;
+  const bool vec = a.V % VE == 0 && a.ldx % VE == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
+                   (!grad || (a.ldg % VE == 0 && reinterpret_cast<uintptr_t>(a.g) % 16 == 0));
+  const bool half = a.V <= 8 * L;
+  if (vec) return half ? launch_lanes_shape<T, MODE, L, 8, true>(a, st)
+                       : launch_lanes_shape<T, MODE, L, 16, true>(a, st);
+  return half ? launch_lanes_shape<T, MODE, L, 8, false>(a, st)
+              : launch_lanes_shape<T, MODE, L, 16, false>(a, st);
+}
+
+// False where the row is too long for these kernels.
 template <typename T, int MODE>
 bool launch_lanes(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
-  const int V = a.V;
-  int L = V <= 8 ? 1 : V <= 16 ? 2 : V <= 32 ? 4 : V <= 64 ? 8 : V <= 128 ? 16 : 32;
-  if (V > 256) return false;
-  if (MODE == LM_DISTILL)
-    while (L < 32 && 32 / L * (TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float) > 48 * 1024)
-      L *= 2;
+  if (a.V > LANES_V_MAX) return false;
+  int L = 1;
+  while (a.V > 16 * L) L *= 2;
+  if (MODE == LM_DISTILL) {
+    // a lane holds its first entries in registers, and 48 KB hold a warp's rows
+    const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float);
+    while (L < 32 && (a.k > TEACHER_AHEAD * L || 32 / L * row > 48 * 1024)) L *= 2;
+  }
   switch (L) {
-    case 1: e = launch_lanes_shape<T, MODE, 1, 8>(a, st); break;
-    case 2: e = launch_lanes_shape<T, MODE, 2, 8>(a, st); break;
-    case 4: e = launch_lanes_shape<T, MODE, 4, 8>(a, st); break;
-    case 8: e = launch_lanes_shape<T, MODE, 8, 8>(a, st); break;
-    case 16: e = launch_lanes_shape<T, MODE, 16, 8>(a, st); break;
-    default: e = launch_lanes_shape<T, MODE, 32, 8>(a, st); break;
+    case 1: e = launch_lanes_of<T, MODE, 1>(a, st); break;
+    case 2: e = launch_lanes_of<T, MODE, 2>(a, st); break;
+    case 4: e = launch_lanes_of<T, MODE, 4>(a, st); break;
+    case 8: e = launch_lanes_of<T, MODE, 8>(a, st); break;
+    case 16: e = launch_lanes_of<T, MODE, 16>(a, st); break;
+    default: e = launch_lanes_of<T, MODE, 32>(a, st); break;
   }
   return true;
 }

@@ -126,6 +126,13 @@ __device__ __forceinline__ Part part_of(const T* x, int V, int rank, int cl) {
   return p;
 }
 
+// Row i of a pass.  The second pass of the preference loss runs backwards: what
+// the first read last is still in L2.
+template <int MODE>
+__device__ __forceinline__ int pass_row(int i, int rows) {
+  return MODE == LM_SCALED ? rows - 1 - i : i;
+}
+
 // Heads of a unit's rows, loaded a row ahead.
 template <int MODE>
 struct HeadStream {
@@ -133,7 +140,7 @@ struct HeadStream {
   float next_w;
   __device__ void load(const RowArgs& a, int r, int rows) {
     if (r >= rows) return;
-    next = load_head<MODE>(a, r);
+    next = load_head<MODE>(a, pass_row<MODE>(r, rows));
     if (MODE == LM_SCALED) next_w = a.wseq[next.b];
   }
   // Rows that do not count, and rows of weight 0, are not read.
@@ -217,7 +224,7 @@ __device__ __forceinline__ void ring_copier(const RowArgs& a, unsigned char* rin
         bool blank;
         heads.take(a, w, blank);
         if (!blank) {
-          const T* x = row_at<T>(a.x, r, a.ldx);
+          const T* x = row_at<T>(a.x, pass_row<MODE>(r, pl.rows), a.ldx);
           const Part p = part_of(x, a.V, pl.rank, pl.cl);
           src = reinterpret_cast<const unsigned char*>(x + p.sp.head) + (size_t)p.lo * 16;
           left = p.n * 16;
@@ -322,7 +329,8 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
   Cursor cur{0, 0};
   Turn turn{0, 0};
   const f32x2 sl2 = pair(a.sl, a.sl);
-  for (int r = pl.first; r < pl.rows; r += pl.units) {
+  for (int i = pl.first; i < pl.rows; i += pl.units) {
+    const int r = pass_row<MODE>(i, pl.rows);
     const T* x = row_at<T>(a.x, r, a.ldx);
     T* g = row_at<T>(a.g, r, a.ldg);
     const Part p = part_of(x, a.V, pl.rank, pl.cl);
@@ -438,11 +446,12 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
   };
   TeacherAhead ahead{};
   int ahead_row = -1;  // the row that `ahead` is of
-  for (int r = pl.first; r < pl.rows; r += pl.units) {
+  for (int i = pl.first; i < pl.rows; i += pl.units) {
+    const int r = pass_row<MODE>(i, pl.rows);
     float w;
     bool blank;
     const Head h = heads.take(a, w, blank);
-    heads.load(a, r + pl.units, pl.rows);
+    heads.load(a, i + pl.units, pl.rows);
     const T* x = row_at<T>(a.x, r, a.ldx);
     T* g = GRAD ? row_at<T>(a.g, r, a.ldg) : nullptr;
     const Part p = part_of(x, a.V, pl.rank, pl.cl);
@@ -647,6 +656,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   }
   __syncthreads();
   if (pl.cl > 1) cluster_sync();
+  if (MODE == LM_SCALED) after_previous();
 
   if (warp == RING_WARPS + groups) {
     pl.first = first;
@@ -707,21 +717,35 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   void (*kern)(const RowArgs, const RingShape) =
       grad ? (void (*)(const RowArgs, const RingShape))loss_ring_kernel<T, MODE, MODE != LM_PREFERENCE>
            : (void (*)(const RowArgs, const RingShape))loss_ring_kernel<T, MODE, MODE == LM_SCALED>;
-  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // once a device and kernel: the attribute stays
+  static std::atomic<uint64_t> raised[2];
+  int dev = 0;
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return true;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(raised[grad].load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, RING_SMEM);
+    if (e != cudaSuccess) return true;
+    raised[grad].fetch_or(bit, std::memory_order_relaxed);
+  }
   const long long rows = (long long)a.B * a.T;
   const long long want = (rows + groups - 1) / groups * s.cl;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3((RING_WARPS + groups + 1) * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = s.cl;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[1] = {};
   cfg.attrs = at;
-  cfg.numAttrs = s.cl > 1 ? 1 : 0;
+  if (s.cl > 1) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = s.cl;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  } else if (MODE == LM_SCALED) {  // never on a cluster
+    at[0] = follows();
+    cfg.numAttrs = 1;
+  }
   // one CTA an SM; clusters only as many as run at once (a GPC need not hold a
   // multiple of cl SMs, and a second wave would take as long as the first)
   int fit = loss_sm_count();

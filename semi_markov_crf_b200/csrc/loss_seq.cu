@@ -56,6 +56,7 @@ __device__ __forceinline__ void logistic(double u, double smoothing, double& los
 __global__ void __launch_bounds__(SUM_THREADS) loss_sums_kernel(SeqArgs a) {
   __shared__ double red[SUM_THREADS / 32];
   const int b = blockIdx.x, tid = threadIdx.x;
+  after_previous();
   const int L = a.lengths[b];
   const bool bad = L < 0 || L > a.T;
   if (bad && tid == 0) set_status(a.status, ST_BAD_LENGTH);
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(SUM_THREADS) loss_sums_kernel(SeqArgs a) {
 __global__ void __launch_bounds__(SUM_THREADS) loss_pairs_kernel(SeqArgs a) {
   __shared__ double red[SUM_THREADS / 32];
   const int i = blockIdx.x, P = a.B / 2, tid = threadIdx.x;
+  after_previous();
   double reward[2], inv[2];
   bool bad = false;
   for (int side = 0; side < 2; ++side) {
@@ -155,14 +157,27 @@ __global__ void preference_scores_kernel(const double* __restrict__ chosen,
   if (grad_rejected) grad_rejected[i] = -g;
 }
 
+namespace {
+
+cudaError_t launch_after(void (*kern)(SeqArgs), int grid, const SeqArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(SUM_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute at = follows();
+  cfg.attrs = &at;
+  cfg.numAttrs = a.T > 0 ? 1 : 0;  // without rows no kernel came before
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace
+
 cudaError_t launch_loss_sums(const SeqArgs& a, cudaStream_t st) {
-  loss_sums_kernel<<<a.B, SUM_THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(loss_sums_kernel, a.B, a, st);
 }
 
 cudaError_t launch_loss_pairs(const SeqArgs& a, cudaStream_t st) {
-  loss_pairs_kernel<<<a.B / 2, SUM_THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(loss_pairs_kernel, a.B / 2, a, st);
 }
 
 cudaError_t launch_policy_scores(const double* logp, const double* old_logp, const double* ref,

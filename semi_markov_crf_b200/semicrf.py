@@ -468,10 +468,14 @@ def _logit_rows(logits, lengths, name="logits"):
 
 
 def _shaped(t, dtype, name, device, shape):
+    try:  # the common case in one go: these calls are short
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index \
+                and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
     _need(t, dtype, name, device)
-    if t.shape != shape:
-        raise TypeError(f"{name} must have shape {tuple(shape)}")
-    return t
+    raise TypeError(f"{name} must have shape {tuple(shape)}")
 
 
 def _loss_out(out, name, shape, dtype, device):
@@ -509,11 +513,11 @@ def _loss_ws(ws, B, T, device):
 def _launch(fn, where, device, *args):
     """Calls fn(*args, stream) with `device` current."""
     index = device.index
-    if index is None or index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc:
         _check(rc, where)
 
