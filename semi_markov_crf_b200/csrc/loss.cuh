@@ -30,6 +30,7 @@ struct RowArgs {
   const int32_t* labels;  // [B, T], negative: does not count (not for LM_DISTILL)
   float sl;             // log2(e) / temperature
   double s;             // 1 / temperature
+  double tau;           // temperature
   double inv_sl;        // 1 / sl
   const float* grad_logp;  // LM_LOGPROB: d loss / d logp [B, T] (nullptr: ones)
   const float* old_logp;   // LM_POLICY
@@ -49,6 +50,11 @@ struct RowArgs {
   float2* stat;            // [B, T] LM_PREFERENCE: a row's base and sum of exponentials
   float* wseq;             // [B] LM_SCALED: d loss / d logp of the sequence's positions
   int* status;             // cleared by the pass (nullptr: left alone)
+  // One position a sequence (T = 1): the pass writes the sequences' sums itself.
+  int single;
+  float* seq_sum;          // [B] each nullable
+  float* seq_kl;
+  int32_t* seq_clipped;
 };
 
 // Workspace of the loss entry points: the status word first, as in the

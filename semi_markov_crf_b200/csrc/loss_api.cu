@@ -82,6 +82,7 @@ int prepare_rows(const void* logits, int dtype, int64_t ld, const int32_t* lengt
   a.add = (flags & SEMICRF_FLAG_ACCUMULATE) ? 1 : 0;
   a.lengths = lengths;
   a.s = 1.0 / temperature;
+  a.tau = temperature;
   a.sl = (float)(LOG2E_D / temperature);
   a.inv_sl = 1.0 / (double)a.sl;
   a.status = p.status;
@@ -97,14 +98,24 @@ int run_rows(int mode, int dtype, const RowArgs& a, cudaStream_t st) {
   return launch_loss_rows(mode, dtype, a, st) == cudaSuccess ? SEMICRF_OK : SEMICRF_ERR_CUDA;
 }
 
-int run_sums(const RowArgs& a, const LossWs& p, const float* tok, float* sum, float* kl_sum,
-             int32_t* clipped, cudaStream_t st) {
+// The rows, then the sums over each sequence (which the row pass writes itself
+// where a sequence has one position).
+int run_rows_and_sums(int mode, int dtype, RowArgs& a, const LossWs& p, float* sum, float* kl_sum,
+                      int32_t* clipped, cudaStream_t st) {
+  if (a.T == 1) {
+    a.single = 1;
+    a.seq_sum = sum;
+    a.seq_kl = kl_sum;
+    a.seq_clipped = clipped;
+  }
+  const int rc = run_rows(mode, dtype, a, st);
+  if (rc || a.single) return rc;
   SeqArgs q{};
   q.B = a.B;
   q.T = a.T;
   q.lengths = a.lengths;
   q.status = p.status;
-  q.tok = tok;
+  q.tok = a.tok;
   q.kl = p.kl;
   q.clip = p.clip;
   q.sum = sum;
@@ -166,8 +177,7 @@ extern "C" int semicrf_label_logprob(const void* logits, int dtype, int64_t ld,
   a.grad_logp = grad_logp;
   a.logp = logp;
   a.tok = p.tok;
-  const int rr = run_rows(LM_LOGPROB, dtype, a, st);
-  return rr ? rr : run_sums(a, p, p.tok, score, nullptr, nullptr, st);
+  return run_rows_and_sums(LM_LOGPROB, dtype, a, p, score, nullptr, nullptr, st);
 }
 
 extern "C" int semicrf_policy_loss(const void* logits, int dtype, int64_t ld,
@@ -201,8 +211,7 @@ extern "C" int semicrf_policy_loss(const void* logits, int dtype, int64_t ld,
   a.tok = p.tok;
   a.kl = kl ? p.kl : nullptr;
   a.clip = clipped ? p.clip : nullptr;
-  const int rr = run_rows(LM_POLICY, dtype, a, st);
-  return rr ? rr : run_sums(a, p, p.tok, loss, kl, clipped, st);
+  return run_rows_and_sums(LM_POLICY, dtype, a, p, loss, kl, clipped, st);
 }
 
 extern "C" int semicrf_preference_loss(const void* logits, int dtype, int64_t ld,
@@ -280,8 +289,7 @@ extern "C" int semicrf_distill_loss(const void* logits, int dtype, int64_t ld,
   a.k = k;
   a.w = grad_loss;
   a.tok = token_loss ? token_loss : p.tok;
-  const int rr = run_rows(LM_DISTILL, dtype, a, st);
-  return rr ? rr : run_sums(a, p, a.tok, loss, nullptr, nullptr, st);
+  return run_rows_and_sums(LM_DISTILL, dtype, a, p, loss, nullptr, nullptr, st);
 }
 
 extern "C" int semicrf_policy_scores(const double* logp, const double* old_logp,

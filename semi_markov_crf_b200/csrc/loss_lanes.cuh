@@ -30,7 +30,8 @@ struct LaneMap {
   }
 };
 
-template <typename T, int MODE, int L, int NE, bool VEC>
+// SHORT: the teacher's entries are at most one a lane and stay in its registers.
+template <typename T, int MODE, int L, int NE, bool VEC, bool SHORT>
 __global__ void __launch_bounds__(LANES_THREADS, LANES_CTAS)
     loss_lanes_kernel(const __grid_constant__ RowArgs a) {
   using Map = LaneMap<T, L, NE, VEC>;
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(LANES_THREADS, LANES_CTAS)
   const int rows = a.B * a.T;  // <= 2^27
   const int units = (int)(gridDim.x * (blockDim.x / L));
   int r = (int)(blockIdx.x * (blockDim.x / L) + tid / L);
-  if (blockIdx.x == 0 && tid == 0 && a.status) *a.status = 0;
+  start_status(a);
   if (r >= rows) return;
   const unsigned mm = L == 32 ? FULL_MASK : ((1u << (L & 31)) - 1u) << ((tid & 31) / L * L);
   const Range all{0, V, V};
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(LANES_THREADS, LANES_CTAS)
     float2 stat;
     LabelIn<T> in;
     LaneRow<T, NE, VEC> x;
-    TeacherAhead ahead;
+    TeacherLoad<SHORT ? 1 : TEACHER_AHEAD> ahead;
   };
   auto start = [&](Load& l, const HeadLoad& head, int row) {
     l.h = make_head<MODE>(a, head);
@@ -77,7 +78,11 @@ __global__ void __launch_bounds__(LANES_THREADS, LANES_CTAS)
     }
     if (MODE == LM_SCALED) l.stat = a.stat[row];
     if (has_label(MODE) && MODE != LM_SCALED) l.in = load_label<T, MODE>(a, row, l.h, x);
-    if (MODE == LM_DISTILL) l.ahead.load(a, row, 0, lane, L);
+    if (MODE == LM_DISTILL) {
+      l.ahead.load(a, row, 0, lane, L);
+      if (a.w) l.in.w = a.w[l.h.b];
+      else l.in.w = 1.0;
+    }
   };
 
   Load now;
@@ -96,8 +101,24 @@ __global__ void __launch_bounds__(LANES_THREADS, LANES_CTAS)
     bool blank = now.blank || (MODE == LM_SCALED && now.w == 0.0f);
     bool malformed = now.blank && now.h.live;
     TeacherHead th{};
+    float tx = 0.0f;
     if (MODE == LM_DISTILL && !blank) {
-      th = teacher_head<T>(a, r, tc, now.ahead, x, g, all, lane, L, mm);
+      if constexpr (SHORT) {
+        const int id = now.ahead.id[0];
+        if (id >= 0 && id < V) {
+          tx = to_f32<T>(x[id]);
+        } else {
+          now.ahead.t[0] = NEG_INF;
+        }
+        th.malformed = lanes_max(id >= V ? 1.0f : 0.0f, L, mm) > 0.0f;
+        const float m = lanes_max(now.ahead.t[0], L, mm);
+        th.tm = m == NEG_INF ? 0.0f : m;
+        const bool used = id >= 0 && id < V;
+        teacher_total(a, r, lanes_sum(used ? expf((now.ahead.t[0] - th.tm) * (float)a.s) : 0.0f, L, mm),
+                      th);
+      } else {
+        th = teacher_head<T>(a, r, tc, now.ahead, x, g, all, lane, L, mm);
+      }
       blank = malformed = th.malformed;
     }
     if (blank) {
@@ -148,20 +169,29 @@ __global__ void __launch_bounds__(LANES_THREADS, LANES_CTAS)
       S = lanes_sum((part[0] + part[1]) + (part[2] + part[3]), L, mm);
     }
 
+    float tp = 0.0f;  // SHORT: the entry's probability
     float cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
     if (MODE == LM_SCALED) {
       cy = (float)((double)now.w * a.s);
       cq = -cy;
     } else if (MODE == LM_DISTILL) {
       P = th.P;
-      teacher_terms(a, r, tc, th, base, S, true, lane, L, mm);
-      cq = (float)((a.w ? a.w[now.h.b] : 1.0) / a.s);
+      if constexpr (SHORT) {
+        float part = 0.0f;
+        tp = now.ahead.id[0] >= 0
+                 ? teacher_p(a, th, base, log2f(S), now.ahead.t[0], tx, part) : 0.0f;
+        part = lanes_sum(part, L, mm);
+        if (lane == 0) put_term(a, r, (float)(a.tau * a.tau) * part);
+      } else {
+        teacher_terms(a, r, tc, th, base, S, true, lane, L, mm);
+      }
+      cq = (float)(now.in.w * a.tau);
     } else {
       cy = label_outputs<MODE>(a, r, now.in, base, S, lane == 0);
       cq = -cy;
     }
     if (g) {
-      const float scale = cq * P / S;
+      const float scale = __fdividef(cq * P, S);
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         v[i] *= scale;
@@ -193,28 +223,48 @@ __global__ void __launch_bounds__(LANES_THREADS, LANES_CTAS)
         }
       }
       if (MODE == LM_DISTILL) {
+        float old = 0.0f;
+        const int id = SHORT ? now.ahead.id[0] : -1;
         __syncwarp(mm);  // the row is written; its teacher entries follow
-        teacher_fix<T>(a, tc, g, base, scale, cq, th.repeats, lane, L, all);
+        if constexpr (SHORT) {
+          // the first of the lanes with one label takes the sum over them, in order
+          const unsigned same = __match_any_sync(mm, id);
+          const int first = __ffs(same) - 1;
+          float p = 0.0f;
+          for (unsigned left = same; __any_sync(mm, left != 0); left &= left - 1) {
+            const int from = left ? __ffs(left) - 1 : (tid & 31);
+            const float other = __shfl_sync(mm, tp, from);
+            if (left) p += other;
+          }
+          if (id >= 0 && first == (tid & 31)) {
+            // where the call accumulates, the row's own term is in already
+            if (a.add) old = to_f32<T>(g[id]);
+            g[id] = from_f32<T>(a.add ? old - cq * p : based_exp(tx, a.sl, base) * scale - cq * p);
+          }
+          __syncwarp(mm);
+        } else {
+          teacher_fix<T>(a, tc, g, base, scale, cq, th.repeats, lane, L, all);
+        }
       }
     }
-    if (MODE == LM_DISTILL) __syncwarp(mm);
+    if (MODE == LM_DISTILL && !SHORT) __syncwarp(mm);
     now = next;
   }
 }
 
-template <typename T, int MODE, int L, int NE, bool VEC>
+template <typename T, int MODE, int L, int NE, bool VEC, bool SHORT>
 cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
   // 48 KB of shared memory for the teacher's entries: fewer rows a CTA where k is large
   int threads = LANES_THREADS;
   size_t smem = 0;
-  if (MODE == LM_DISTILL) {
+  if (MODE == LM_DISTILL && !SHORT) {
     const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float);
     while (threads > 32 && threads / L * row > 48 * 1024) threads /= 2;
     smem = threads / L * row;
   }
   const long long rows = (long long)a.B * a.T, per = threads / L;
   const long long fit = (long long)loss_sm_count() * LANES_CTAS * (LANES_THREADS / threads);
-  loss_lanes_kernel<T, MODE, L, NE, VEC>
+  loss_lanes_kernel<T, MODE, L, NE, VEC, SHORT>
       <<<(unsigned)std::min(fit, (rows + per - 1) / per), threads, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -226,10 +276,17 @@ cudaError_t launch_lanes_of(const RowArgs& a, cudaStream_t st) {
   const bool vec = a.V % VE == 0 && a.ldx % VE == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
                    (!grad || (a.ldg % VE == 0 && reinterpret_cast<uintptr_t>(a.g) % 16 == 0));
   const bool half = a.V <= 8 * L;
-  if (vec) return half ? launch_lanes_shape<T, MODE, L, 8, true>(a, st)
-                       : launch_lanes_shape<T, MODE, L, 16, true>(a, st);
-  return half ? launch_lanes_shape<T, MODE, L, 8, false>(a, st)
-              : launch_lanes_shape<T, MODE, L, 16, false>(a, st);
+  auto shape = [&](auto one_a_lane) {
+    constexpr bool SHORT = decltype(one_a_lane)::value;
+    if (vec) return half ? launch_lanes_shape<T, MODE, L, 8, true, SHORT>(a, st)
+                         : launch_lanes_shape<T, MODE, L, 16, true, SHORT>(a, st);
+    return half ? launch_lanes_shape<T, MODE, L, 8, false, SHORT>(a, st)
+                : launch_lanes_shape<T, MODE, L, 16, false, SHORT>(a, st);
+  };
+  if constexpr (MODE == LM_DISTILL) {
+    if (a.k <= L) return shape(std::true_type{});
+  }
+  return shape(std::false_type{});
 }
 
 // False where the row is too long for these kernels.
@@ -241,7 +298,7 @@ bool launch_lanes(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   if (MODE == LM_DISTILL) {
     // a lane holds its first entries in registers, and 48 KB hold a warp's rows
     const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float);
-    while (L < 32 && (a.k > TEACHER_AHEAD * L || 32 / L * row > 48 * 1024)) L *= 2;
+    while (L < 32 && (a.k > L || 32 / L * row > 48 * 1024)) L *= 2;
   }
   switch (L) {
     case 1: e = launch_lanes_of<T, MODE, 1>(a, st); break;

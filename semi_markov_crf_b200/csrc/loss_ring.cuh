@@ -543,12 +543,12 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
       } else if (MODE == LM_DISTILL) {
         P = th.P;
         zero = th.malformed;
-        cq = (float)((a.w ? a.w[h.b] : 1.0) / a.s);
+        cq = (float)((a.w ? a.w[h.b] : 1.0) * a.tau);
       } else {
         cy = label_outputs<MODE>(a, r, in, base, S, lane == 0 && pl.rank == 0);
         cq = -cy;
       }
-      const float scale = cq * P / S;
+      const float scale = __fdividef(cq * P, S);
       if (GRAD) {
         note.at = base.at;
         note.scale = scale;
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   float* teachers = reinterpret_cast<float*>(states + groups);
   const int first = (int)(blockIdx.x / pl.cl) * groups;
 
-  if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = 0;
+  start_status(a);
   if (threadIdx.x < groups) {
     GroupState& st = states[threadIdx.x];
     for (int i = 0; i < pl.slots; ++i) {
@@ -683,11 +683,33 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   }
 }
 
-// Warps a group.
-inline int ring_warps(size_t row_bytes) {
-  int W = 2;
-  while (W < RING_WARPS && row_bytes > (size_t)W * 8 * 1024) W *= 2;
-  return W;
+// A kernel's limits on a device, asked for once.
+struct RingLimits {
+  std::atomic<uint64_t> raised{0};                       // devices whose shared-memory limit is raised
+  std::atomic<int> clusters[RING_CLUSTER_MAX + 1][8]{};  // resident clusters of each size, device < 8
+};
+
+// Clusters of `cl` CTAs that run at once (a GPC need not hold a multiple of cl
+// SMs: of 148 SMs clusters of 4 reach 132, clusters of 8 reach 120).
+template <typename K>
+cudaError_t resident_clusters(K kern, RingLimits& lim, int dev, int cl, int& n) {
+  n = loss_sm_count();
+  if (cl == 1) return cudaSuccess;
+  if (dev < 8 && (n = lim.clusters[cl][dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(loss_sm_count() / cl * cl);
+  cfg.blockDim = dim3(RING_THREADS);
+  cfg.dynamicSmemBytes = RING_SMEM;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = cl;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+  n = std::max(n, 1);
+  if (e == cudaSuccess && dev < 8) lim.clusters[cl][dev].store(n, std::memory_order_relaxed);
+  return e;
 }
 
 // False where a row with a gradient does not fit the rings of a cluster.
@@ -696,10 +718,34 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   const bool grad = a.g != nullptr && MODE != LM_PREFERENCE;
   const bool hold = grad && MODE != LM_SCALED;  // the row stays in the ring between the passes
   const size_t row = (size_t)a.V * sizeof(T);
-  const size_t entry = MODE == LM_DISTILL ? (2ull * TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float) : 0;
+  const size_t entry =
+      MODE == LM_DISTILL ? (2ull * TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float) : 0;
+  const long long rows = (long long)a.B * a.T;
+  static RingLimits limits[2];
+  RingLimits& lim = limits[grad];
+  void (*kern)(const RowArgs, const RingShape) =
+      grad ? (void (*)(const RowArgs, const RingShape))loss_ring_kernel<T, MODE, MODE != LM_PREFERENCE>
+           : (void (*)(const RowArgs, const RingShape))loss_ring_kernel<T, MODE, MODE == LM_SCALED>;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return true;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(lim.raised.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, RING_SMEM);
+    if (e != cudaSuccess) return true;
+    lim.raised.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int sms = loss_sm_count();
+
+  // Warps a group: 8 KB of a row for each (rows in flight hide one another's
+  // latency), all 16 where there are too few rows for more groups.
   RingShape s;
-  s.W = ring_warps(row);
-  while (s.W < RING_WARPS && RING_WARPS / s.W * entry > 40 * 1024) s.W *= 2;
+  s.W = 2;
+  while (s.W < RING_WARPS &&
+         (row > (size_t)s.W * 8 * 1024 || rows <= (long long)sms * (RING_WARPS / s.W) / 2 ||
+          RING_WARPS / s.W * entry > 40 * 1024))
+    s.W *= 2;
   size_t chunk, fixed;
   for (;; s.W *= 2) {
     const int groups = RING_WARPS / s.W;
@@ -712,51 +758,39 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   if (hold)
     while (s.cl <= RING_CLUSTER_MAX && row > (size_t)s.cl * (s.slots - 1) * chunk) ++s.cl;
   if (s.cl > RING_CLUSTER_MAX) return false;
-  const int groups = RING_WARPS / s.W;
-  const size_t smem = groups * s.slots * chunk + fixed;
-  void (*kern)(const RowArgs, const RingShape) =
-      grad ? (void (*)(const RowArgs, const RingShape))loss_ring_kernel<T, MODE, MODE != LM_PREFERENCE>
-           : (void (*)(const RowArgs, const RingShape))loss_ring_kernel<T, MODE, MODE == LM_SCALED>;
-  // once a device and kernel: the attribute stays
-  static std::atomic<uint64_t> raised[2];
-  int dev = 0;
-  e = cudaGetDevice(&dev);
+  int resident;
+  e = resident_clusters(kern, lim, dev, s.cl, resident);
   if (e != cudaSuccess) return true;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!(raised[grad].load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, RING_SMEM);
-    if (e != cudaSuccess) return true;
-    raised[grad].fetch_or(bit, std::memory_order_relaxed);
+  if (s.W == RING_WARPS && rows * s.cl * 2 <= sms) {
+    // a handful of rows: each is spread over as many CTAs as they leave, 4 KB at least
+    for (int cl = RING_CLUSTER_MAX; cl > s.cl; --cl) {
+      int n;
+      if (row < (size_t)cl * 4096) continue;
+      e = resident_clusters(kern, lim, dev, cl, n);
+      if (e != cudaSuccess) return true;
+      if (rows <= n) {
+        s.cl = cl;
+        resident = n;
+        break;
+      }
+    }
   }
-  const long long rows = (long long)a.B * a.T;
-  const long long want = (rows + groups - 1) / groups * s.cl;
+  const int groups = RING_WARPS / s.W;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3((RING_WARPS + groups + 1) * 32);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = groups * s.slots * chunk + fixed;
   cfg.stream = st;
-  cudaLaunchAttribute at[1] = {};
+  cudaLaunchAttribute at[2] = {};
   cfg.attrs = at;
   if (s.cl > 1) {
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = s.cl;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.numAttrs = 1;
-  } else if (MODE == LM_SCALED) {  // never on a cluster
-    at[0] = follows();
-    cfg.numAttrs = 1;
   }
-  // one CTA an SM; clusters only as many as run at once (a GPC need not hold a
-  // multiple of cl SMs, and a second wave would take as long as the first)
-  int fit = loss_sm_count();
-  if (s.cl > 1) {
-    cfg.gridDim = dim3((unsigned)(fit / s.cl * s.cl));
-    int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-    if (e != cudaSuccess) return true;
-    fit = std::max(1, clusters) * s.cl;
-  }
-  cfg.gridDim = dim3((unsigned)std::min<long long>(want, fit));
+  if (MODE == LM_SCALED) at[cfg.numAttrs++] = follows();
+  const long long want = (rows + groups - 1) / groups;
+  cfg.gridDim = dim3((unsigned)(std::min<long long>(want, resident) * s.cl));
   e = cudaLaunchKernelEx(&cfg, kern, a, s);
   return true;
 }

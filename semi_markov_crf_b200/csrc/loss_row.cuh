@@ -172,16 +172,43 @@ __device__ __forceinline__ LabelIn<T> load_label(const RowArgs& a, long long r, 
   return in;
 }
 
+// The pass starts with a clear status word.  With one position a sequence there
+// is no pass over the sequences that would look at the lengths, so the first
+// CTA does.  Called by all threads of every CTA.
+__device__ __forceinline__ void start_status(const RowArgs& a) {
+  if (blockIdx.x != 0 || !a.status) return;
+  int bad = 0;
+  if (a.single)
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) bad |= a.lengths[b] < 0 || a.lengths[b] > a.T;
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *a.status = bad ? ST_BAD_LENGTH : 0;
+}
+
+// A position's term, and its sequence's sum where that is all of it.
+__device__ __forceinline__ void put_term(const RowArgs& a, long long r, float v) {
+  if (a.tok) a.tok[r] = v;
+  if (a.single && a.seq_sum) a.seq_sum[r] = v;
+}
+__device__ __forceinline__ void put_policy(const RowArgs& a, long long r, float kl, bool clipped) {
+  if (a.kl) a.kl[r] = kl;
+  if (a.clip) a.clip[r] = clipped;
+  if (a.single && a.seq_kl) a.seq_kl[r] = kl;
+  if (a.single && a.seq_clipped) a.seq_clipped[r] = clipped;
+}
+
 // The outputs of a position that does not count, or whose labels are malformed.
 template <int MODE>
 __device__ __forceinline__ void blank_outputs(const RowArgs& a, long long r, bool malformed) {
-  const float v = malformed ? quiet_nan() : 0.0f;
-  if (a.tok) a.tok[r] = v;
+  float v = malformed ? quiet_nan() : 0.0f;
   if (has_label(MODE) && a.logp) a.logp[r] = v;
-  if (MODE == LM_POLICY) {
-    if (a.kl) a.kl[r] = v;
-    if (a.clip) a.clip[r] = 0;
+  if (MODE == LM_DISTILL && a.tok) a.tok[r] = v;
+  if (a.single && (a.lengths[r] < 0 || a.lengths[r] > a.T)) v = quiet_nan();
+  if (MODE == LM_DISTILL) {
+    if (a.single && a.seq_sum) a.seq_sum[r] = v;
+  } else {
+    put_term(a, r, v);
   }
+  if (MODE == LM_POLICY) put_policy(a, r, v, false);
 }
 
 // What follows from a row's base and sum for a label loss: the position's
@@ -200,13 +227,10 @@ __device__ __forceinline__ float label_outputs(const RowArgs& a, long long r, co
                            (float)((double)in.ref_logp - logp));
     term = o.loss;
     slope = o.slope;
-    if (writer) {
-      if (a.kl) a.kl[r] = o.kl;
-      if (a.clip) a.clip[r] = o.clipped;
-    }
+    if (writer) put_policy(a, r, o.kl, o.clipped);
   }
   if (writer) {
-    if (a.tok) a.tok[r] = term;
+    put_term(a, r, term);
     if (a.logp) a.logp[r] = (float)logp;
     if (MODE == LM_PREFERENCE) a.stat[r] = pack_stat(h, S);
   }
@@ -259,18 +283,44 @@ __device__ __forceinline__ float lanes_sum(float v, int n, unsigned mm) {
 
 // The first TEACHER_AHEAD entries of each lane, loaded before they are needed.
 constexpr int TEACHER_AHEAD = 4;
-struct TeacherAhead {
-  int id[TEACHER_AHEAD];
-  float t[TEACHER_AHEAD];
+template <int U>
+struct TeacherLoad {
+  int id[U];
+  float t[U];
   __device__ __forceinline__ void load(const RowArgs& a, long long r, int from, int lane, int n) {
 #pragma unroll
-    for (int u = 0; u < TEACHER_AHEAD; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int j = from + u * n + lane;
       id[u] = j < a.k ? a.ids[r * a.k + j] : -1;
       t[u] = j < a.k ? a.tl[r * a.k + j] : NEG_INF;
     }
   }
 };
+using TeacherAhead = TeacherLoad<TEACHER_AHEAD>;
+
+// log-sum-exp and total probability of a teacher whose greatest logit is tm
+// and whose exponentials around it sum to s.
+__device__ __forceinline__ void teacher_total(const RowArgs& a, long long r, float s, TeacherHead& th) {
+  if (a.tlse) {
+    th.tlog = (float)((double)a.tlse[r] - (double)th.tm * a.s);
+    th.P = s * expf(-th.tlog);
+  } else {
+    th.tlog = logf(s);
+    th.P = s > 0.0f ? 1.0f : s;  // no entry with a probability: no loss, no gradient
+  }
+}
+
+// An entry's probability and its term of the loss, log p - log q taken from
+// differences with both maxima.
+__device__ __forceinline__ float teacher_p(const RowArgs& a, const TeacherHead& th, const Base& h,
+                                           float log2S, float t, float x, float& part) {
+  if (t == NEG_INF) return 0.0f;
+  const float lt = fmaf(t - th.tm, (float)a.s, -th.tlog);
+  const float p = expf(lt);
+  const float lq = (h.direct ? fmaf(x, a.sl, -h.at) : (x - h.at) * a.sl) - log2S;
+  if (p != 0.0f) part += p * fmaf(lq, -(float)LN2_D, lt);
+  return p;
+}
 
 // Takes the entries in (the first ones are in `ahead`); the maximum and
 // log-sum-exp of the teacher's logits over those in use.
@@ -311,13 +361,7 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
   for (int j = lane; j < a.k; j += n)
     if (tc.id[j] >= 0) s += expf((tc.p[j] - th.tm) * st);
   s = lanes_sum(s, n, mm);
-  if (a.tlse) {
-    th.tlog = (float)((double)a.tlse[r] - (double)th.tm * a.s);
-    th.P = s * expf(-th.tlog);
-  } else {
-    th.tlog = logf(s);
-    th.P = s > 0.0f ? 1.0f : s;  // no entry with a probability: no loss, no gradient
-  }
+  teacher_total(a, r, s, th);
   th.repeats = true;
   const int size = teacher_table(a.k);
   if (size) {
@@ -343,22 +387,14 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
 __device__ __forceinline__ void teacher_terms(const RowArgs& a, long long r, const Teacher& tc,
                                               const TeacherHead& th, const Base& h, float S,
                                               bool loss, int lane, int n, unsigned mm) {
-  const double logS = log_of_sum(S), m = base_score(h, a.inv_sl);
+  const float log2S = log2f(S);
   float part = 0.0f;
-  for (int j = lane; j < a.k; j += n) {
-    float p = 0.0f;
-    if (tc.id[j] >= 0 && tc.p[j] != NEG_INF) {
-      const float lt = (float)((double)(tc.p[j] - th.tm) * a.s - (double)th.tlog);
-      p = expf(lt);
-      if (p != 0.0f) part += p * (lt - (float)(((double)tc.x[j] - m) * a.s - logS));
-    }
-    tc.p[j] = p;
-  }
+  for (int j = lane; j < a.k; j += n)
+    tc.p[j] = tc.id[j] >= 0 ? teacher_p(a, th, h, log2S, tc.p[j], tc.x[j], part) : 0.0f;
   __syncwarp(mm);
   if (loss) {
     part = lanes_sum(part, n, mm);
-    const double tau = 1.0 / a.s;
-    if (lane == 0) a.tok[r] = (float)(tau * tau * (double)part);
+    if (lane == 0) put_term(a, r, (float)(a.tau * a.tau) * part);
   }
 }
 

@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
   extern __shared__ float dyn[];
   const long long r = blockIdx.x;
   const int tid = threadIdx.x, V = a.V, warp = tid >> 5, lane = tid & 31;
-  if (r == 0 && tid == 0 && a.status) *a.status = 0;
+  start_status(a);
   const Head h = make_head<MODE>(a, load_head<MODE>(a, r));
   const T* x = row_at<T>(a.x, r, a.ldx);
   T* g = a.g ? row_at<T>(a.g, r, a.ldg) : nullptr;
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
     if (MODE == LM_DISTILL) {
       P = tshare[0];
       if (warp == 0) teacher_terms(a, r, tc, th, base, S, true, lane, 32, FULL_MASK);
-      cq = (float)((a.w ? a.w[h.b] : 1.0) / a.s);
+      cq = (float)((a.w ? a.w[h.b] : 1.0) * a.tau);
       if (a.add) __syncthreads();  // the gradient's old values at the entries are read
     } else {
       cy = label_outputs<MODE>(a, r, load_label<T, MODE>(a, r, h, x), base, S, tid == 0);
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
     }
   }
   if (!g || MODE == LM_PREFERENCE) return;
-  const float scale = cq * P / S;
+  const float scale = __fdividef(cq * P, S);
   for (int v = tid; v < V; v += WIDE_THREADS) {
     float gv = based_exp(to_f32<T>(x[v]), a.sl, base) * scale;
     if (has_label(MODE) && v == h.y) gv += cy;
