@@ -2,10 +2,10 @@
 // sums over a sequence's positions, the paired loss, and the path forms of
 // both (one score per segmentation).
 //
-//   loss_sums_kernel    one CTA per sequence: the float64 sums of the
-//                       per-position terms in a fixed order; a bad length goes
-//                       to the status word, which the row pass cleared.
-//   loss_pairs_kernel   one CTA per pair: S = sum of logp - ref of both
+//   loss_sums_kernel    a CTA, or a cluster, per sequence: the float64 sums of
+//                       the per-position terms in a fixed order; a bad length
+//                       goes to the status word, which the row pass cleared.
+//   loss_pairs_kernel   a CTA, or a cluster, per pair: S = sum of logp - ref of both
 //                       sequences (or its mean), the logistic loss on
 //                       u = beta (S_c - S_r) - margin, and the weight of each
 //                       sequence's positions for the gradient pass.
@@ -14,28 +14,83 @@
 //                       log Z that feed them and take their gradients.
 // The arrays are B * T floats against the rows' B * T * V: a few microseconds
 // of latency, not bandwidth, is what these cost.
+#include <algorithm>
+
 #include "loss.cuh"
 
 namespace semicrf {
 
 namespace {
 
-constexpr int SUM_THREADS = 256;
+constexpr int SUM_THREADS = 1024;  // at most
+constexpr int SUM_CTAS = 8;        // of a cluster, at most
+constexpr int SUM_UNROLL = 8;      // independent loads a thread has in flight
 
-__device__ __forceinline__ double warp_sum(double v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
-  return v;
+// Threads and CTAs for sequences of T positions: one sweep of the loads covers
+// most sequences, and a long one is spread over a cluster (T = 10^6 with one
+// CTA of 256 threads, a load at a time, took 0.5 ms).
+struct SumShape {
+  int threads, ctas;
+};
+inline SumShape sum_shape(int T) {
+  SumShape s{T <= 2048 ? 256 : SUM_THREADS, 1};
+  const long long per = (long long)s.threads * SUM_UNROLL;
+  s.ctas = (int)std::min<long long>(SUM_CTAS, std::max<long long>(1, (T + per - 1) / per));
+  return s;
 }
 
-// Sum over the CTA in a fixed order, in every thread.
-__device__ __forceinline__ double cta_sum(double v, double* red) {
-  v = warp_sum(v);
-  __syncthreads();  // red may still be read from the sum before
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+struct SumState {
+  double warp[3][SUM_THREADS / 32];
+  double cta[SUM_CTAS][3];
+};
+
+// Sums of up to three per-position arrays over t < n, split over the CTAs of
+// the cluster, in a fixed order; complete in every thread of CTA 0.  `value`:
+// (array, position) -> double.  Every thread of every CTA calls it.
+template <int N, typename F>
+__device__ __forceinline__ void sequence_sums(int n, int rank, int ctas, SumState& st, F value,
+                                              double (&out)[N]) {
+  const int threads = blockDim.x, tid = threadIdx.x;
+  double s[N] = {};
+  for (long long t0 = (long long)rank * threads * SUM_UNROLL + tid; t0 < n;
+       t0 += (long long)ctas * threads * SUM_UNROLL) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      double v[SUM_UNROLL];
+#pragma unroll
+      for (int u = 0; u < SUM_UNROLL; ++u) {
+        const long long t = t0 + (long long)u * threads;
+        v[u] = t < n ? value(k, (int)t) : 0.0;
+      }
+#pragma unroll
+      for (int u = 0; u < SUM_UNROLL; ++u) s[k] += v[u];
+    }
+  }
+  __syncthreads();  // the state may still be read from the sums before
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    double v = s[k];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+    if ((tid & 31) == 0) st.warp[k][tid >> 5] = v;
+  }
   __syncthreads();
-  double s = 0.0;
-  for (int i = 0; i < SUM_THREADS / 32; ++i) s += red[i];
-  return s;
+  if (tid < N) {
+    double v = 0.0;
+    for (int i = 0; i < threads / 32; ++i) v += st.warp[tid][i];
+    // to CTA 0 of the cluster
+    uint32_t to = smem_addr(&st.cta[rank][tid]);
+    if (ctas > 1) to = cluster_addr(&st.cta[rank][tid], 0);
+    if (ctas > 1) asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(v) : "memory");
+    else st.cta[0][tid] = v;
+  }
+  __syncthreads();
+  if (ctas > 1) cluster_sync();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    out[k] = 0.0;
+    if (rank == 0)
+      for (int i = 0; i < ctas; ++i) out[k] += st.cta[i][k];
+  }
 }
 
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
@@ -53,70 +108,59 @@ __device__ __forceinline__ void logistic(double u, double smoothing, double& los
 
 }  // namespace
 
-__global__ void __launch_bounds__(SUM_THREADS) loss_sums_kernel(SeqArgs a) {
-  __shared__ double red[SUM_THREADS / 32];
-  const int b = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(SUM_THREADS) loss_sums_kernel(SeqArgs a, int ctas) {
+  __shared__ SumState st;
+  const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas;
+  if (ctas > 1) cluster_sync();  // the peers are running
   after_previous();
   const int L = a.lengths[b];
   const bool bad = L < 0 || L > a.T;
-  if (bad && tid == 0) set_status(a.status, ST_BAD_LENGTH);
-  const int n = bad ? 0 : L;
   const long long row = (long long)b * a.T;
-  double s = 0.0, k = 0.0, c = 0.0;
-  for (int t = tid; t < n; t += SUM_THREADS) {
-    s += (double)a.tok[row + t];
-    if (a.kl_sum) k += (double)a.kl[row + t];
-    if (a.clipped) c += (double)a.clip[row + t];
-  }
-  if (a.sum) {
-    s = cta_sum(s, red);
-    if (tid == 0) a.sum[b] = bad ? quiet_nan() : (float)s;
-  }
-  if (a.kl_sum) {
-    k = cta_sum(k, red);
-    if (tid == 0) a.kl_sum[b] = bad ? quiet_nan() : (float)k;
-  }
-  if (a.clipped) {
-    c = cta_sum(c, red);
-    if (tid == 0) a.clipped[b] = (int32_t)c;
-  }
+  double out[3];
+  sequence_sums<3>(bad ? 0 : L, rank, ctas, st, [&](int k, int t) -> double {
+    if (k == 0) return a.sum ? (double)a.tok[row + t] : 0.0;
+    if (k == 1) return a.kl_sum ? (double)a.kl[row + t] : 0.0;
+    return a.clipped ? (double)a.clip[row + t] : 0.0;
+  }, out);
+  if (rank != 0 || threadIdx.x != 0) return;
+  if (bad) set_status(a.status, ST_BAD_LENGTH);
+  if (a.sum) a.sum[b] = bad ? quiet_nan() : (float)out[0];
+  if (a.kl_sum) a.kl_sum[b] = bad ? quiet_nan() : (float)out[1];
+  if (a.clipped) a.clipped[b] = (int32_t)out[2];
 }
 
-__global__ void __launch_bounds__(SUM_THREADS) loss_pairs_kernel(SeqArgs a) {
-  __shared__ double red[SUM_THREADS / 32];
-  const int i = blockIdx.x, P = a.B / 2, tid = threadIdx.x;
+__global__ void __launch_bounds__(SUM_THREADS) loss_pairs_kernel(SeqArgs a, int ctas) {
+  __shared__ SumState st;
+  const int i = blockIdx.x / ctas, rank = blockIdx.x - i * ctas, P = a.B / 2;
+  if (ctas > 1) cluster_sync();  // the peers are running
   after_previous();
   double reward[2], inv[2];
-  bool bad = false;
+  bool off[2];
   for (int side = 0; side < 2; ++side) {
     const int b = i + side * P;
     const int L = a.lengths[b];
-    const bool off = L < 0 || L > a.T;
-    bad |= off;
-    if (off && tid == 0) set_status(a.status, ST_BAD_LENGTH);
-    const int n = off ? 0 : L;
+    off[side] = L < 0 || L > a.T;
     const long long row = (long long)b * a.T;
-    double s = 0.0, c = 0.0;
-    for (int t = tid; t < n; t += SUM_THREADS) {
-      s += (double)a.tok[row + t];
-      if (a.average) c += a.labels[row + t] >= 0 ? 1.0 : 0.0;
-    }
-    s = cta_sum(s, red);
-    c = a.average ? cta_sum(c, red) : 1.0;
-    inv[side] = 1.0 / fmax(c, 1.0);
-    reward[side] = a.beta * s * inv[side];
+    double out[2];
+    sequence_sums<2>(off[side] ? 0 : L, rank, ctas, st, [&](int k, int t) -> double {
+      if (k == 0) return (double)a.tok[row + t];
+      return a.average && a.labels[row + t] >= 0 ? 1.0 : 0.0;
+    }, out);
+    if (ctas > 1) cluster_sync();  // CTA 0 has read the other side's sums
+    inv[side] = 1.0 / fmax(out[1], 1.0);
+    reward[side] = a.beta * out[0] * inv[side];
   }
-  if (tid != 0) return;
+  if (rank != 0 || threadIdx.x != 0) return;
   double loss, slope;
   logistic(reward[0] - reward[1] - a.margin, a.smoothing, loss, slope);
   const double w = (a.w ? a.w[i] : 1.0) * a.beta * slope;
   // a pair with a malformed sequence has loss NaN and no gradient
-  const bool none = bad || loss != loss;
+  const bool none = off[0] || off[1] || loss != loss;
+  if (off[0] || off[1]) set_status(a.status, ST_BAD_LENGTH);
   if (a.loss) a.loss[i] = none ? quiet_nan() : (float)loss;
   for (int side = 0; side < 2; ++side) {
     const int b = i + side * P;
-    const bool off = a.lengths[b] < 0 || a.lengths[b] > a.T;
-    if (a.reward) a.reward[b] = off ? quiet_nan() : (float)reward[side];
+    if (a.reward) a.reward[b] = off[side] ? quiet_nan() : (float)reward[side];
     a.wseq[b] = none ? 0.0f : (float)(side ? -w * inv[1] : w * inv[0]);
   }
 }
@@ -159,15 +203,23 @@ __global__ void preference_scores_kernel(const double* __restrict__ chosen,
 
 namespace {
 
-cudaError_t launch_after(void (*kern)(SeqArgs), int grid, const SeqArgs& a, cudaStream_t st) {
+cudaError_t launch_after(void (*kern)(SeqArgs, int), int sequences, const SeqArgs& a,
+                         cudaStream_t st) {
+  const SumShape shape = sum_shape(a.T);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(SUM_THREADS);
+  cfg.gridDim = dim3((unsigned)sequences * shape.ctas);
+  cfg.blockDim = dim3(shape.threads);
   cfg.stream = st;
-  cudaLaunchAttribute at = follows();
-  cfg.attrs = &at;
-  cfg.numAttrs = a.T > 0 ? 1 : 0;  // without rows no kernel came before
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  cudaLaunchAttribute at[2] = {};
+  cfg.attrs = at;
+  if (a.T > 0) at[cfg.numAttrs++] = follows();  // without rows no kernel came before
+  if (shape.ctas > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = shape.ctas;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, a, shape.ctas);
 }
 
 }  // namespace
