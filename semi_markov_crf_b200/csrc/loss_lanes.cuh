@@ -11,17 +11,18 @@
 // elements.
 
 constexpr int LANES_THREADS = 128;
-constexpr int LANES_CTAS = 7;  // an SM, by registers
-constexpr int LANES_V_MAX = 512;
+constexpr int LANES_V_MAX = 2048;
+constexpr int LANES_SHORT = 2;  // teacher's entries a lane keeps in registers
+constexpr int lanes_ctas(int NE) { return NE > 32 ? 4 : NE > 16 ? 8 : 10; }  // an SM, by registers
 
-// A row as loaded.
+// A row as loaded: 16-byte vectors, or elements.
 template <typename T, int NE, bool VEC>
 struct LaneRow {
   uint4 q[VEC ? NE / vec_of<T> : 1];
   T e[VEC ? 1 : NE];
 };
 
-template <typename T, int L, int NE, bool VEC>
+template <typename T, int L, bool VEC>
 struct LaneMap {
   static constexpr int VE = VEC ? vec_of<T> : 1;
   // element of this lane's i-th
@@ -30,226 +31,267 @@ struct LaneMap {
   }
 };
 
-// SHORT: the teacher's entries are at most one a lane and stay in its registers.
-template <typename T, int MODE, int L, int NE, bool VEC, bool SHORT>
-__global__ void __launch_bounds__(LANES_THREADS, LANES_CTAS)
-    loss_lanes_kernel(const __grid_constant__ RowArgs a) {
-  using Map = LaneMap<T, L, NE, VEC>;
+// The row at hand and what is on its way for it.
+template <typename T, int NE, bool VEC, int AHEAD>
+struct LaneLoad {
+  Head h;
+  bool blank;
+  float w;
+  float2 stat;
+  LabelIn<T> in;
+  LaneRow<T, NE, VEC> x;
+  TeacherLoad<AHEAD> ahead;
+};
+
+template <typename T, int MODE, int L, int NE, bool VEC, int AHEAD>
+__device__ __forceinline__ void lane_load(const RowArgs& a, LaneLoad<T, NE, VEC, AHEAD>& l,
+                                          const HeadLoad& head, int row, int lane) {
+  using Map = LaneMap<T, L, VEC>;
   constexpr int VE = vec_of<T>;
+  l.h = make_head<MODE>(a, head);
+  l.w = MODE == LM_SCALED && l.h.live ? a.wseq[l.h.b] : 0.0f;
+  l.blank = !l.h.live || l.h.malformed;
+  if (l.blank) return;
+  const T* x = row_at<T>(a.x, row, a.ldx);
+  // past the row: -inf, whose exponential is 0 around any base of a row that has one
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < NE / VE; ++i) {
+      constexpr uint32_t none = Vec<T>::LOWEST;
+      l.x.q[i] = make_uint4(none, none, none, none);
+      if (Map::at(i * VE, lane) < a.V) l.x.q[i] = __ldg(reinterpret_cast<const uint4*>(x) + (i * L + lane));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      l.x.e[i] = from_f32<T>(NEG_INF);
+      if (Map::at(i, lane) < a.V) l.x.e[i] = x[Map::at(i, lane)];
+    }
+  }
+  if (MODE == LM_SCALED) l.stat = a.stat[row];
+  if (has_label(MODE) && MODE != LM_SCALED) l.in = load_label<T, MODE>(a, row, l.h, x);
+  if (MODE == LM_DISTILL) {
+    l.ahead.load(a, row, 0, lane, L);
+    l.in.w = a.w ? a.w[l.h.b] : 1.0;
+  }
+}
+
+// One row.  SHORT: the teacher's entries are at most LANES_SHORT a lane and
+// stay in its registers.
+template <typename T, int MODE, int L, int NE, bool VEC, bool SHORT, int AHEAD>
+__device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, AHEAD>& now, int r,
+                                         const Teacher& tc, int lane, unsigned mm) {
+  using Map = LaneMap<T, L, VEC>;
+  constexpr int VE = vec_of<T>;
+  const int V = a.V;
+  const T* x = row_at<T>(a.x, r, a.ldx);
+  T* g = a.g && MODE != LM_PREFERENCE ? row_at<T>(a.g, r, a.ldg) : nullptr;
+  const Range all{0, V, V};
+  bool blank = now.blank || (MODE == LM_SCALED && now.w == 0.0f);
+  bool malformed = now.blank && now.h.live;
+  TeacherHead th{};
+  float tx[AHEAD], tp[AHEAD];  // SHORT: the row's scores at the entries, their probabilities
+  if (MODE == LM_DISTILL && !blank) {
+    if constexpr (SHORT) {
+      float m = NEG_INF, out = 0.0f, s = 0.0f;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int id = now.ahead.id[u];
+        if (id >= V) out = 1.0f;
+        if (id < 0 || id >= V) now.ahead.t[u] = NEG_INF;
+        tx[u] = id >= 0 && id < V ? to_f32<T>(x[id]) : 0.0f;
+        m = fmaxf(m, now.ahead.t[u]);
+      }
+      th.malformed = lanes_max(out, L, mm) > 0.0f;
+      m = lanes_max(m, L, mm);
+      th.tm = m == NEG_INF ? 0.0f : m;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (now.ahead.id[u] >= 0) s += expf((now.ahead.t[u] - th.tm) * (float)a.s);
+      teacher_total(a, a.tlse ? a.tlse[r] : 0.0f, lanes_sum(s, L, mm), th);
+    } else {
+      th = teacher_head<T>(a, r, tc, now.ahead, x, g, all, lane, L, mm);
+    }
+    blank = malformed = th.malformed;
+  }
+  if (blank) {
+    if (MODE != LM_SCALED && lane == 0) blank_outputs<MODE>(a, r, malformed);
+    if (g && !a.add)
+      for (int v = lane; v < V; v += L) g[v] = from_f32<T>(0.0f);
+    return;
+  }
+
+  f32x2 v[NE / 2];
+  float top = NEG_INF;
+  if constexpr (VEC) {
+    top = Vec<T>::greatest(now.x.q);
+#pragma unroll
+    for (int i = 0; i < NE / VE; ++i) {
+      f32x2 two[VE / 2];
+      Vec<T>::unpack(now.x.q[i], two);
+#pragma unroll
+      for (int e = 0; e < VE / 2; ++e) v[i * (VE / 2) + e] = two[e];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE / 2; ++i) {
+      const float lo = to_f32<T>(now.x.e[2 * i]), hi = to_f32<T>(now.x.e[2 * i + 1]);
+      top = fmaxf(top, fmaxf(lo, hi));
+      v[i] = pair(lo, hi);
+    }
+  }
+  Base base;
+  float S = 0.0f;
+  if (MODE == LM_SCALED) {
+    base = unpack_stat(now.stat, S);
+  } else {
+    base = make_base(lanes_max(top, L, mm), a.sl);
+  }
+  if (base.direct) {
+    const f32x2 sl2 = pair(a.sl, a.sl), at2 = pair(-base.at, -base.at);
+#pragma unroll
+    for (int i = 0; i < NE / 2; ++i) v[i] = ex2_2(fma2(v[i], sl2, at2));
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE / 2; ++i) {
+      float lo, hi;
+      halves(v[i], lo, hi);
+      v[i] = pair(ex2((lo - base.at) * a.sl), ex2((hi - base.at) * a.sl));
+    }
+  }
+  if (MODE != LM_SCALED) {
+    f32x2 part[2] = {v[0], v[1]};
+#pragma unroll
+    for (int i = 2; i < NE / 2; ++i) part[i & 1] = add2(part[i & 1], v[i]);
+    float lo, hi;
+    halves(add2(part[0], part[1]), lo, hi);
+    S = lanes_sum(lo + hi, L, mm);
+  }
+
+  float cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
+  if (MODE == LM_SCALED) {
+    cy = (float)((double)now.w * a.s);
+    cq = -cy;
+  } else if (MODE == LM_DISTILL) {
+    P = th.P;
+    if constexpr (SHORT) {
+      const float log2S = log2f(S);
+      float part = 0.0f;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        tp[u] = now.ahead.id[u] >= 0 ? teacher_p(a, th, base, log2S, now.ahead.t[u], tx[u], part) : 0.0f;
+      part = lanes_sum(part, L, mm);
+      if (lane == 0) put_term(a, r, (float)(a.tau * a.tau) * part);
+    } else {
+      teacher_terms(a, r, tc, th, base, S, true, lane, L, mm);
+    }
+    cq = (float)(now.in.w * a.tau);
+  } else {
+    cy = label_outputs<MODE>(a, r, now.in, base, S, lane == 0);
+    cq = -cy;
+  }
+  if (!g) return;
+  const float scale = __fdividef(cq * P, S);
+  const f32x2 scale2 = pair(scale, scale);
+#pragma unroll
+  for (int i = 0; i < NE / 2; ++i) v[i] = mul2(v[i], scale2);
+  if constexpr (VEC) {
+    uint4* out = reinterpret_cast<uint4*>(g);
+#pragma unroll
+    for (int i = 0; i < NE / VE; ++i) {
+      if (Map::at(i * VE, lane) >= V) continue;
+      f32x2 two[VE / 2];
+#pragma unroll
+      for (int e = 0; e < VE / 2; ++e) two[e] = v[i * (VE / 2) + e];
+      if (sizeof(T) == 4 && a.add) {
+        f32x2 old[VE / 2];
+        Vec<T>::unpack(out[i * L + lane], old);
+#pragma unroll
+        for (int e = 0; e < VE / 2; ++e) two[e] = add2(two[e], old[e]);
+      }
+      out[i * L + lane] = Vec<T>::pack(two);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE / 2; ++i) {
+      float gv[2];
+      halves(v[i], gv[0], gv[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int at = Map::at(2 * i + e, lane);
+        if (at >= V) continue;
+        if (a.add) gv[e] += to_f32<T>(g[at]);
+        g[at] = from_f32<T>(gv[e]);
+      }
+    }
+  }
+  __syncwarp(mm);  // the row is written; its label or teacher's entries follow
+  if (has_label(MODE)) {
+    if (lane == 0) {
+      const T score = MODE == LM_SCALED ? x[now.h.y] : now.in.score;
+      const float gv = based_exp(to_f32<T>(score), a.sl, base) * scale + cy;
+      g[now.h.y] = from_f32<T>(a.add ? to_f32<T>(g[now.h.y]) + cy : gv);
+    }
+  } else if constexpr (SHORT) {
+    // entries of one label add up, in order, into the first of them
+    float sum[AHEAD];
+    bool first[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      sum[u] = 0.0f;
+      first[u] = now.ahead.id[u] >= 0;
+    }
+    for (int s = 0; s < a.k; ++s) {
+      const int from = s % L, slot = s / L;
+      int id = now.ahead.id[0];
+      float p = tp[0];
+#pragma unroll
+      for (int u = 1; u < AHEAD; ++u)
+        if (slot == u) {
+          id = now.ahead.id[u];
+          p = tp[u];
+        }
+      id = __shfl_sync(mm, id, from, L);
+      p = __shfl_sync(mm, p, from, L);
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (id == now.ahead.id[u]) {
+          if (s < u * L + lane) first[u] = false;
+          sum[u] += p;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (first[u]) {
+        const int id = now.ahead.id[u];
+        // where the call accumulates, the row's own term is in already
+        const float own = a.add ? to_f32<T>(g[id]) : based_exp(tx[u], a.sl, base) * scale;
+        g[id] = from_f32<T>(own - cq * sum[u]);
+      }
+  } else {
+    teacher_fix<T>(a, tc, g, base, scale, cq, th.repeats, lane, L, all);
+    __syncwarp(mm);  // the entries' shared memory is the next row's
+  }
+}
+
+template <typename T, int MODE, int L, int NE, bool VEC, bool SHORT>
+__global__ void __launch_bounds__(LANES_THREADS, lanes_ctas(NE))
+    loss_lanes_kernel(const __grid_constant__ RowArgs a) {
+  constexpr int AHEAD = SHORT ? LANES_SHORT : TEACHER_AHEAD;
   extern __shared__ float dyn[];
-  const int tid = threadIdx.x, V = a.V, lane = tid % L;
+  const int tid = threadIdx.x, lane = tid % L;
   const int rows = a.B * a.T;  // <= 2^27
-  const int units = (int)(gridDim.x * (blockDim.x / L));
-  int r = (int)(blockIdx.x * (blockDim.x / L) + tid / L);
+  const int r = (int)(blockIdx.x * (blockDim.x / L) + tid / L);
   start_status(a);
   if (r >= rows) return;
   const unsigned mm = L == 32 ? FULL_MASK : ((1u << (L & 31)) - 1u) << ((tid & 31) / L * L);
-  const Range all{0, V, V};
-  float* mine =
-      dyn + (size_t)(tid / L) * (MODE == LM_DISTILL ? TEACHER_WORDS * a.k + teacher_table(a.k) : 0);
+  float* mine = dyn + (size_t)(tid / L) *
+                          (MODE == LM_DISTILL && !SHORT ? TEACHER_WORDS * a.k + teacher_table(a.k) : 0);
   const Teacher tc{mine, reinterpret_cast<int*>(mine + a.k), mine + 2 * a.k, mine + 3 * a.k,
                    reinterpret_cast<int*>(mine + TEACHER_WORDS * a.k)};
-
-  // the row at hand and what is on its way for it
-  struct Load {
-    Head h;
-    bool blank;
-    float w;
-    float2 stat;
-    LabelIn<T> in;
-    LaneRow<T, NE, VEC> x;
-    TeacherLoad<SHORT ? 1 : TEACHER_AHEAD> ahead;
-  };
-  auto start = [&](Load& l, const HeadLoad& head, int row) {
-    l.h = make_head<MODE>(a, head);
-    l.w = MODE == LM_SCALED && l.h.live ? a.wseq[l.h.b] : 0.0f;
-    l.blank = !l.h.live || l.h.malformed;
-    if (l.blank) return;
-    const T* x = row_at<T>(a.x, row, a.ldx);
-    if (VEC) {
-#pragma unroll
-      for (int i = 0; i < NE / VE; ++i)
-        if (Map::at(i * VE, lane) < V)
-          l.x.q[i] = __ldg(reinterpret_cast<const uint4*>(x) + (i * L + lane));
-    } else {
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (Map::at(i, lane) < V) l.x.e[i] = x[Map::at(i, lane)];
-    }
-    if (MODE == LM_SCALED) l.stat = a.stat[row];
-    if (has_label(MODE) && MODE != LM_SCALED) l.in = load_label<T, MODE>(a, row, l.h, x);
-    if (MODE == LM_DISTILL) {
-      l.ahead.load(a, row, 0, lane, L);
-      if (a.w) l.in.w = a.w[l.h.b];
-      else l.in.w = 1.0;
-    }
-  };
-
-  Load now;
-  start(now, load_head<MODE>(a, r), r);
-  HeadLoad soon{};
-  if (r + units < rows) soon = load_head<MODE>(a, r + units);
-  for (; r < rows; r += units) {
-    Load next;
-    next.blank = true;
-    if (r + units < rows) {
-      start(next, soon, r + units);
-      if (r + 2 * (long long)units < rows) soon = load_head<MODE>(a, r + 2 * units);
-    }
-    const T* x = row_at<T>(a.x, r, a.ldx);
-    T* g = a.g && MODE != LM_PREFERENCE ? row_at<T>(a.g, r, a.ldg) : nullptr;
-    bool blank = now.blank || (MODE == LM_SCALED && now.w == 0.0f);
-    bool malformed = now.blank && now.h.live;
-    TeacherHead th{};
-    float tx = 0.0f;
-    if (MODE == LM_DISTILL && !blank) {
-      if constexpr (SHORT) {
-        const int id = now.ahead.id[0];
-        if (id >= 0 && id < V) {
-          tx = to_f32<T>(x[id]);
-        } else {
-          now.ahead.t[0] = NEG_INF;
-        }
-        th.malformed = lanes_max(id >= V ? 1.0f : 0.0f, L, mm) > 0.0f;
-        const float m = lanes_max(now.ahead.t[0], L, mm);
-        th.tm = m == NEG_INF ? 0.0f : m;
-        const bool used = id >= 0 && id < V;
-        teacher_total(a, r, lanes_sum(used ? expf((now.ahead.t[0] - th.tm) * (float)a.s) : 0.0f, L, mm),
-                      th);
-      } else {
-        th = teacher_head<T>(a, r, tc, now.ahead, x, g, all, lane, L, mm);
-      }
-      blank = malformed = th.malformed;
-    }
-    if (blank) {
-      if (MODE != LM_SCALED && lane == 0) blank_outputs<MODE>(a, r, malformed);
-      if (g && !a.add)
-        for (int v = lane; v < V; v += L) g[v] = from_f32<T>(0.0f);
-      now = next;
-      continue;
-    }
-
-    float v[NE];
-    if (VEC) {
-#pragma unroll
-      for (int i = 0; i < NE / VE; ++i) {
-        f32x2 two[Vec<T>::PAIRS];
-        Vec<T>::unpack(now.x.q[i], two);
-#pragma unroll
-        for (int e = 0; e < Vec<T>::PAIRS; ++e) halves(two[e], v[i * VE + 2 * e], v[i * VE + 2 * e + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NE; ++i) v[i] = to_f32<T>(now.x.e[i]);
-    }
-
-    Base base;
-    float S = 0.0f;
-    if (MODE == LM_SCALED) {
-      base = unpack_stat(now.stat, S);
-    } else {
-      float m = NEG_INF;
-#pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (Map::at(i, lane) < V) m = fmaxf(m, v[i]);
-      base = make_base(lanes_max(m, L, mm), a.sl);
-    }
-    // past the row: no score, whatever the base is (-inf - -inf is not a number)
-    if (base.direct) {
-#pragma unroll
-      for (int i = 0; i < NE; ++i) v[i] = Map::at(i, lane) < V ? ex2(fmaf(v[i], a.sl, -base.at)) : 0.0f;
-    } else {
-#pragma unroll
-      for (int i = 0; i < NE; ++i) v[i] = Map::at(i, lane) < V ? ex2((v[i] - base.at) * a.sl) : 0.0f;
-    }
-    if (MODE != LM_SCALED) {
-      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < NE; ++i) part[i & 3] += v[i];
-      S = lanes_sum((part[0] + part[1]) + (part[2] + part[3]), L, mm);
-    }
-
-    float tp = 0.0f;  // SHORT: the entry's probability
-    float cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
-    if (MODE == LM_SCALED) {
-      cy = (float)((double)now.w * a.s);
-      cq = -cy;
-    } else if (MODE == LM_DISTILL) {
-      P = th.P;
-      if constexpr (SHORT) {
-        float part = 0.0f;
-        tp = now.ahead.id[0] >= 0
-                 ? teacher_p(a, th, base, log2f(S), now.ahead.t[0], tx, part) : 0.0f;
-        part = lanes_sum(part, L, mm);
-        if (lane == 0) put_term(a, r, (float)(a.tau * a.tau) * part);
-      } else {
-        teacher_terms(a, r, tc, th, base, S, true, lane, L, mm);
-      }
-      cq = (float)(now.in.w * a.tau);
-    } else {
-      cy = label_outputs<MODE>(a, r, now.in, base, S, lane == 0);
-      cq = -cy;
-    }
-    if (g) {
-      const float scale = __fdividef(cq * P, S);
-#pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        v[i] *= scale;
-        if (has_label(MODE) && Map::at(i, lane) == now.h.y) v[i] += cy;
-      }
-      if (VEC) {
-        uint4* out = reinterpret_cast<uint4*>(g);
-#pragma unroll
-        for (int i = 0; i < NE / VE; ++i) {
-          if (Map::at(i * VE, lane) >= V) continue;
-          f32x2 two[Vec<T>::PAIRS];
-#pragma unroll
-          for (int e = 0; e < Vec<T>::PAIRS; ++e) two[e] = pair(v[i * VE + 2 * e], v[i * VE + 2 * e + 1]);
-          if (sizeof(T) == 4 && a.add) {
-            f32x2 old[Vec<T>::PAIRS];
-            Vec<T>::unpack(out[i * L + lane], old);
-#pragma unroll
-            for (int e = 0; e < Vec<T>::PAIRS; ++e) two[e] = add2(two[e], old[e]);
-          }
-          out[i * L + lane] = Vec<T>::pack(two);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          const int e = Map::at(i, lane);
-          if (e >= V) continue;
-          if (a.add) v[i] += to_f32<T>(g[e]);
-          g[e] = from_f32<T>(v[i]);
-        }
-      }
-      if (MODE == LM_DISTILL) {
-        float old = 0.0f;
-        const int id = SHORT ? now.ahead.id[0] : -1;
-        __syncwarp(mm);  // the row is written; its teacher entries follow
-        if constexpr (SHORT) {
-          // the first of the lanes with one label takes the sum over them, in order
-          const unsigned same = __match_any_sync(mm, id);
-          const int first = __ffs(same) - 1;
-          float p = 0.0f;
-          for (unsigned left = same; __any_sync(mm, left != 0); left &= left - 1) {
-            const int from = left ? __ffs(left) - 1 : (tid & 31);
-            const float other = __shfl_sync(mm, tp, from);
-            if (left) p += other;
-          }
-          if (id >= 0 && first == (tid & 31)) {
-            // where the call accumulates, the row's own term is in already
-            if (a.add) old = to_f32<T>(g[id]);
-            g[id] = from_f32<T>(a.add ? old - cq * p : based_exp(tx, a.sl, base) * scale - cq * p);
-          }
-          __syncwarp(mm);
-        } else {
-          teacher_fix<T>(a, tc, g, base, scale, cq, th.repeats, lane, L, all);
-        }
-      }
-    }
-    if (MODE == LM_DISTILL && !SHORT) __syncwarp(mm);
-    now = next;
-  }
+  LaneLoad<T, NE, VEC, AHEAD> row;
+  lane_load<T, MODE, L>(a, row, load_head<MODE>(a, r), r, lane);
+  lane_row<T, MODE, L, NE, VEC, SHORT>(a, row, r, tc, lane, mm);
 }
 
 template <typename T, int MODE, int L, int NE, bool VEC, bool SHORT>
@@ -263,50 +305,58 @@ cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
     smem = threads / L * row;
   }
   const long long rows = (long long)a.B * a.T, per = threads / L;
-  const long long fit = (long long)loss_sm_count() * LANES_CTAS * (LANES_THREADS / threads);
   loss_lanes_kernel<T, MODE, L, NE, VEC, SHORT>
-      <<<(unsigned)std::min(fit, (rows + per - 1) / per), threads, smem, st>>>(a);
+      <<<(unsigned)((rows + per - 1) / per), threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, int MODE, int L>
+// NE: 8, 16 or (vectors only) 32 elements a lane.
+template <typename T, int MODE, int L, bool VEC, bool SHORT>
 cudaError_t launch_lanes_of(const RowArgs& a, cudaStream_t st) {
-  constexpr int VE = vec_of<T>;
-  const bool grad = a.g != nullptr;
-  const bool vec = a.V % VE == 0 && a.ldx % VE == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
-                   (!grad || (a.ldg % VE == 0 && reinterpret_cast<uintptr_t>(a.g) % 16 == 0));
-  const bool half = a.V <= 8 * L;
-  auto shape = [&](auto one_a_lane) {
-    constexpr bool SHORT = decltype(one_a_lane)::value;
-    if (vec) return half ? launch_lanes_shape<T, MODE, L, 8, true, SHORT>(a, st)
-                         : launch_lanes_shape<T, MODE, L, 16, true, SHORT>(a, st);
-    return half ? launch_lanes_shape<T, MODE, L, 8, false, SHORT>(a, st)
-                : launch_lanes_shape<T, MODE, L, 16, false, SHORT>(a, st);
-  };
-  if constexpr (MODE == LM_DISTILL) {
-    if (a.k <= L) return shape(std::true_type{});
+  if (a.V <= 8 * L) return launch_lanes_shape<T, MODE, L, 8, VEC, SHORT>(a, st);
+  if (a.V <= 16 * L) return launch_lanes_shape<T, MODE, L, 16, VEC, SHORT>(a, st);
+  if constexpr (VEC && L < 32) return launch_lanes_shape<T, MODE, L, 32, VEC, SHORT>(a, st);
+  if constexpr (L == 32) {
+    if (a.V <= 32 * L) return launch_lanes_shape<T, MODE, L, 32, VEC, SHORT>(a, st);
+    return launch_lanes_shape<T, MODE, L, 64, VEC, SHORT>(a, st);
   }
-  return shape(std::false_type{});
+  return cudaErrorInvalidValue;  // not reached: L is chosen by V
+}
+
+template <typename T, int MODE, bool VEC, bool SHORT>
+cudaError_t launch_lanes_with(const RowArgs& a, int L, cudaStream_t st) {
+  switch (L) {
+    case 1: return launch_lanes_of<T, MODE, 1, VEC, SHORT>(a, st);
+    case 2: return launch_lanes_of<T, MODE, 2, VEC, SHORT>(a, st);
+    case 4: return launch_lanes_of<T, MODE, 4, VEC, SHORT>(a, st);
+    case 8: return launch_lanes_of<T, MODE, 8, VEC, SHORT>(a, st);
+    case 16: return launch_lanes_of<T, MODE, 16, VEC, SHORT>(a, st);
+    default: return launch_lanes_of<T, MODE, 32, VEC, SHORT>(a, st);
+  }
 }
 
 // False where the row is too long for these kernels.
 template <typename T, int MODE>
 bool launch_lanes(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   if (a.V > LANES_V_MAX) return false;
+  constexpr int VE = vec_of<T>;
+  const bool grad = a.g != nullptr;
+  const bool vec = a.V % VE == 0 && a.ldx % VE == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
+                   (!grad || (a.ldg % VE == 0 && reinterpret_cast<uintptr_t>(a.g) % 16 == 0));
   int L = 1;
-  while (a.V > 16 * L) L *= 2;
-  if (MODE == LM_DISTILL) {
+  while (L < 32 && a.V > (vec ? 32 : 16) * L) L *= 2;
+  if constexpr (MODE == LM_DISTILL) {
+    if (a.k <= TEACHER_SHORT) {
+      while (a.k > LANES_SHORT * L) L *= 2;
+      e = vec ? launch_lanes_with<T, MODE, true, true>(a, L, st)
+              : launch_lanes_with<T, MODE, false, true>(a, L, st);
+      return true;
+    }
     // a lane holds its first entries in registers, and 48 KB hold a warp's rows
     const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float);
-    while (L < 32 && (a.k > L || 32 / L * row > 48 * 1024)) L *= 2;
+    while (L < 32 && (a.k > TEACHER_AHEAD * L || 32 / L * row > 48 * 1024)) L *= 2;
   }
-  switch (L) {
-    case 1: e = launch_lanes_of<T, MODE, 1>(a, st); break;
-    case 2: e = launch_lanes_of<T, MODE, 2>(a, st); break;
-    case 4: e = launch_lanes_of<T, MODE, 4>(a, st); break;
-    case 8: e = launch_lanes_of<T, MODE, 8>(a, st); break;
-    case 16: e = launch_lanes_of<T, MODE, 16>(a, st); break;
-    default: e = launch_lanes_of<T, MODE, 32>(a, st); break;
-  }
+  e = vec ? launch_lanes_with<T, MODE, true, false>(a, L, st)
+          : launch_lanes_with<T, MODE, false, false>(a, L, st);
   return true;
 }

@@ -300,9 +300,9 @@ using TeacherAhead = TeacherLoad<TEACHER_AHEAD>;
 
 // log-sum-exp and total probability of a teacher whose greatest logit is tm
 // and whose exponentials around it sum to s.
-__device__ __forceinline__ void teacher_total(const RowArgs& a, long long r, float s, TeacherHead& th) {
+__device__ __forceinline__ void teacher_total(const RowArgs& a, float lse, float s, TeacherHead& th) {
   if (a.tlse) {
-    th.tlog = (float)((double)a.tlse[r] - (double)th.tm * a.s);
+    th.tlog = (float)((double)lse - (double)th.tm * a.s);
     th.P = s * expf(-th.tlog);
   } else {
     th.tlog = logf(s);
@@ -361,7 +361,7 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
   for (int j = lane; j < a.k; j += n)
     if (tc.id[j] >= 0) s += expf((tc.p[j] - th.tm) * st);
   s = lanes_sum(s, n, mm);
-  teacher_total(a, r, s, th);
+  teacher_total(a, a.tlse ? a.tlse[r] : 0.0f, s, th);
   th.repeats = true;
   const int size = teacher_table(a.k);
   if (size) {
