@@ -12,7 +12,6 @@
 
 constexpr int LANES_THREADS = 128;
 constexpr int LANES_V_MAX = 2048;
-constexpr int LANES_SHORT = 2;  // teacher's entries a lane keeps in registers
 constexpr int lanes_ctas(int NE) { return NE > 32 ? 4 : NE > 16 ? 8 : 10; }  // an SM, by registers
 
 // A row as loaded: 16-byte vectors, or elements.
@@ -76,13 +75,14 @@ __device__ __forceinline__ void lane_load(const RowArgs& a, LaneLoad<T, NE, VEC,
   }
 }
 
-// One row.  SHORT: the teacher's entries are at most LANES_SHORT a lane and
-// stay in its registers.
-template <typename T, int MODE, int L, int NE, bool VEC, bool SHORT, int AHEAD>
+// One row.  KEEP: teacher's entries that a lane keeps in registers; 0: they go
+// through shared memory (lists of more than 128).
+template <typename T, int MODE, int L, int NE, bool VEC, int KEEP, int AHEAD>
 __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, AHEAD>& now, int r,
                                          const Teacher& tc, int lane, unsigned mm) {
   using Map = LaneMap<T, L, VEC>;
   constexpr int VE = vec_of<T>;
+  constexpr bool SHORT = KEEP > 0;
   const int V = a.V;
   const T* x = row_at<T>(a.x, r, a.ldx);
   T* g = a.g && MODE != LM_PREFERENCE ? row_at<T>(a.g, r, a.ldg) : nullptr;
@@ -241,7 +241,30 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, 
       sum[u] = 0.0f;
       first[u] = now.ahead.id[u] >= 0;
     }
-    for (int s = 0; s < a.k; ++s) {
+    bool repeats = true;
+    const int size = teacher_table(a.k);
+    if (size) {
+      // longer lists: a hash table tells whether a label comes twice at all (half
+      // empty, so that every probe ends)
+      for (int s = lane; s < size; s += L) tc.table[s] = -1;
+      __syncwarp(mm);
+      float twice = 0.0f;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int id = now.ahead.id[u];
+        if (id < 0) continue;
+        for (unsigned at = (unsigned)id * 2654435769u;; ++at) {
+          const int was = atomicCAS(&tc.table[at & (size - 1)], -1, id);
+          if (was == id) twice = 1.0f;
+          if (was == -1 || was == id) break;
+        }
+      }
+      repeats = lanes_max(twice, L, mm) > 0.0f;
+      if (!repeats)
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) sum[u] = tp[u];
+    }
+    for (int s = 0; repeats && s < a.k; ++s) {
       const int from = s % L, slot = s / L;
       int id = now.ahead.id[0];
       float p = tp[0];
@@ -274,10 +297,10 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, 
   }
 }
 
-template <typename T, int MODE, int L, int NE, bool VEC, bool SHORT>
+template <typename T, int MODE, int L, int NE, bool VEC, int KEEP>
 __global__ void __launch_bounds__(LANES_THREADS, lanes_ctas(NE))
     loss_lanes_kernel(const __grid_constant__ RowArgs a) {
-  constexpr int AHEAD = SHORT ? LANES_SHORT : TEACHER_AHEAD;
+  constexpr int AHEAD = KEEP ? KEEP : TEACHER_AHEAD;
   extern __shared__ float dyn[];
   const int tid = threadIdx.x, lane = tid % L;
   const int rows = a.B * a.T;  // <= 2^27
@@ -285,54 +308,57 @@ __global__ void __launch_bounds__(LANES_THREADS, lanes_ctas(NE))
   start_status(a);
   if (r >= rows) return;
   const unsigned mm = L == 32 ? FULL_MASK : ((1u << (L & 31)) - 1u) << ((tid & 31) / L * L);
-  float* mine = dyn + (size_t)(tid / L) *
-                          (MODE == LM_DISTILL && !SHORT ? TEACHER_WORDS * a.k + teacher_table(a.k) : 0);
+  const int words = KEEP ? 0 : TEACHER_WORDS * a.k;
+  float* mine = dyn + (size_t)(tid / L) * (MODE == LM_DISTILL ? words + teacher_table(a.k) : 0);
   const Teacher tc{mine, reinterpret_cast<int*>(mine + a.k), mine + 2 * a.k, mine + 3 * a.k,
-                   reinterpret_cast<int*>(mine + TEACHER_WORDS * a.k)};
+                   reinterpret_cast<int*>(mine + words)};
   LaneLoad<T, NE, VEC, AHEAD> row;
   lane_load<T, MODE, L>(a, row, load_head<MODE>(a, r), r, lane);
-  lane_row<T, MODE, L, NE, VEC, SHORT>(a, row, r, tc, lane, mm);
+  lane_row<T, MODE, L, NE, VEC, KEEP>(a, row, r, tc, lane, mm);
 }
 
-template <typename T, int MODE, int L, int NE, bool VEC, bool SHORT>
+template <typename T, int MODE, int L, int NE, bool VEC, int KEEP>
 cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
   // 48 KB of shared memory for the teacher's entries: fewer rows a CTA where k is large
   int threads = LANES_THREADS;
   size_t smem = 0;
-  if (MODE == LM_DISTILL && !SHORT) {
-    const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float);
+  if (MODE == LM_DISTILL) {
+    const size_t row =
+        (size_t)((KEEP ? 0 : TEACHER_WORDS * a.k) + teacher_table(a.k)) * sizeof(float);
     while (threads > 32 && threads / L * row > 48 * 1024) threads /= 2;
     smem = threads / L * row;
   }
   const long long rows = (long long)a.B * a.T, per = threads / L;
-  loss_lanes_kernel<T, MODE, L, NE, VEC, SHORT>
+  loss_lanes_kernel<T, MODE, L, NE, VEC, KEEP>
       <<<(unsigned)((rows + per - 1) / per), threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
 // NE: 8, 16 or (vectors only) 32 elements a lane.
-template <typename T, int MODE, int L, bool VEC, bool SHORT>
+template <typename T, int MODE, int L, bool VEC, int KEEP>
 cudaError_t launch_lanes_of(const RowArgs& a, cudaStream_t st) {
-  if (a.V <= 8 * L) return launch_lanes_shape<T, MODE, L, 8, VEC, SHORT>(a, st);
-  if (a.V <= 16 * L) return launch_lanes_shape<T, MODE, L, 16, VEC, SHORT>(a, st);
-  if constexpr (VEC && L < 32) return launch_lanes_shape<T, MODE, L, 32, VEC, SHORT>(a, st);
+  if (a.V <= 8 * L) return launch_lanes_shape<T, MODE, L, 8, VEC, KEEP>(a, st);
+  if (a.V <= 16 * L) return launch_lanes_shape<T, MODE, L, 16, VEC, KEEP>(a, st);
+  if constexpr (VEC && L < 32) return launch_lanes_shape<T, MODE, L, 32, VEC, KEEP>(a, st);
   if constexpr (L == 32) {
-    if (a.V <= 32 * L) return launch_lanes_shape<T, MODE, L, 32, VEC, SHORT>(a, st);
-    return launch_lanes_shape<T, MODE, L, 64, VEC, SHORT>(a, st);
+    if (a.V <= 32 * L) return launch_lanes_shape<T, MODE, L, 32, VEC, KEEP>(a, st);
+    return launch_lanes_shape<T, MODE, L, 64, VEC, KEEP>(a, st);
   }
   return cudaErrorInvalidValue;  // not reached: L is chosen by V
 }
 
-template <typename T, int MODE, bool VEC, bool SHORT>
+template <typename T, int MODE, bool VEC, int KEEP>
 cudaError_t launch_lanes_with(const RowArgs& a, int L, cudaStream_t st) {
-  switch (L) {
-    case 1: return launch_lanes_of<T, MODE, 1, VEC, SHORT>(a, st);
-    case 2: return launch_lanes_of<T, MODE, 2, VEC, SHORT>(a, st);
-    case 4: return launch_lanes_of<T, MODE, 4, VEC, SHORT>(a, st);
-    case 8: return launch_lanes_of<T, MODE, 8, VEC, SHORT>(a, st);
-    case 16: return launch_lanes_of<T, MODE, 16, VEC, SHORT>(a, st);
-    default: return launch_lanes_of<T, MODE, 32, VEC, SHORT>(a, st);
+  if constexpr (KEEP != 4) {  // long lists come with L = 32
+    switch (L) {
+      case 1: return launch_lanes_of<T, MODE, 1, VEC, KEEP>(a, st);
+      case 2: return launch_lanes_of<T, MODE, 2, VEC, KEEP>(a, st);
+      case 4: return launch_lanes_of<T, MODE, 4, VEC, KEEP>(a, st);
+      case 8: return launch_lanes_of<T, MODE, 8, VEC, KEEP>(a, st);
+      case 16: return launch_lanes_of<T, MODE, 16, VEC, KEEP>(a, st);
+    }
   }
+  return launch_lanes_of<T, MODE, 32, VEC, KEEP>(a, st);
 }
 
 // False where the row is too long for these kernels.
@@ -346,17 +372,22 @@ bool launch_lanes(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   int L = 1;
   while (L < 32 && a.V > (vec ? 32 : 16) * L) L *= 2;
   if constexpr (MODE == LM_DISTILL) {
-    if (a.k <= TEACHER_SHORT) {
-      while (a.k > LANES_SHORT * L) L *= 2;
-      e = vec ? launch_lanes_with<T, MODE, true, true>(a, L, st)
-              : launch_lanes_with<T, MODE, false, true>(a, L, st);
+    if (a.k <= 64) {
+      while (a.k > 2 * L) L *= 2;
+      e = vec ? launch_lanes_with<T, MODE, true, 2>(a, L, st)
+              : launch_lanes_with<T, MODE, false, 2>(a, L, st);
+      return true;
+    }
+    if (a.k <= 128) {
+      e = vec ? launch_lanes_with<T, MODE, true, 4>(a, 32, st)
+              : launch_lanes_with<T, MODE, false, 4>(a, 32, st);
       return true;
     }
     // a lane holds its first entries in registers, and 48 KB hold a warp's rows
     const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float);
     while (L < 32 && (a.k > TEACHER_AHEAD * L || 32 / L * row > 48 * 1024)) L *= 2;
   }
-  e = vec ? launch_lanes_with<T, MODE, true, false>(a, L, st)
-          : launch_lanes_with<T, MODE, false, false>(a, L, st);
+  e = vec ? launch_lanes_with<T, MODE, true, 0>(a, L, st)
+          : launch_lanes_with<T, MODE, false, 0>(a, L, st);
   return true;
 }
