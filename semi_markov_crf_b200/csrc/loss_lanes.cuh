@@ -3,27 +3,33 @@
 //
 // Rows of a few hundred bytes come by the hundred thousand (the emissions of
 // a batch of sequences).  What counts is instructions a row (the scalar work
-// of a position costs as much as its elements) and latency: few lanes a row,
-// so that a warp works on several, reductions of log2 L shuffles, and
-// persistent groups that load the next row and the head after that while they
-// work on this one.  VEC: 16-byte loads and stores (rows on 16-byte
-// boundaries); otherwise element by element, neighbouring lanes neighbouring
-// elements.
+// of a position costs as much as its elements) and rows in flight: few lanes a
+// row, so that a warp works on several at once and a reduction is log2 L
+// shuffles, one row a group, and no more registers than 28 to 40 warps an SM
+// leave.  (Loading a row ahead costs the registers of a third of the warps
+// and was slower: 31 against 21 us for 80000 rows of 128 float32; tiles in
+// shared memory behind TMA copies, 16 warps an SM, took 28.)
+//
+// Layouts: VECTORS, rows on 16-byte boundaries; SPLIT, the 16-byte vectors
+// within a row and up to 14 single elements, one a lane; ELEMENTS, neighbouring
+// lanes neighbouring elements.
 
+enum LaneLayout : int { ELEMENTS = 0, VECTORS = 1, SPLIT = 2 };
 constexpr int LANES_THREADS = 128;
 constexpr int LANES_V_MAX = 2048;
+constexpr int LANES_ELEMENTS = 256;  // longer rows that are not on 16-byte boundaries are split
 constexpr int lanes_ctas(int NE) { return NE > 32 ? 4 : NE > 16 ? 8 : 10; }  // an SM, by registers
 
-// A row as loaded: 16-byte vectors, or elements.
-template <typename T, int NE, bool VEC>
+// A row as loaded: 16-byte vectors, or elements (one beside the vectors where they split).
+template <typename T, int NE, int LAY>
 struct LaneRow {
-  uint4 q[VEC ? NE / vec_of<T> : 1];
-  T e[VEC ? 1 : NE];
+  uint4 q[LAY ? NE / vec_of<T> : 1];
+  T e[LAY ? 1 : NE];
 };
 
-template <typename T, int L, bool VEC>
+template <typename T, int L, int LAY>
 struct LaneMap {
-  static constexpr int VE = VEC ? vec_of<T> : 1;
+  static constexpr int VE = LAY ? vec_of<T> : 1;
   // element of this lane's i-th
   static __device__ __forceinline__ int at(int i, int lane) {
     return (i / VE) * (L * VE) + lane * VE + i % VE;
@@ -31,21 +37,21 @@ struct LaneMap {
 };
 
 // The row at hand and what is on its way for it.
-template <typename T, int NE, bool VEC, int AHEAD>
+template <typename T, int NE, int LAY, int AHEAD>
 struct LaneLoad {
   Head h;
   bool blank;
   float w;
   float2 stat;
   LabelIn<T> in;
-  LaneRow<T, NE, VEC> x;
+  LaneRow<T, NE, LAY> x;
   TeacherLoad<AHEAD> ahead;
 };
 
-template <typename T, int MODE, int L, int NE, bool VEC, int AHEAD>
-__device__ __forceinline__ void lane_load(const RowArgs& a, LaneLoad<T, NE, VEC, AHEAD>& l,
+template <typename T, int MODE, int L, int NE, int LAY, int AHEAD>
+__device__ __forceinline__ void lane_load(const RowArgs& a, LaneLoad<T, NE, LAY, AHEAD>& l,
                                           const HeadLoad& head, int row, int lane) {
-  using Map = LaneMap<T, L, VEC>;
+  using Map = LaneMap<T, L, LAY>;
   constexpr int VE = vec_of<T>;
   l.h = make_head<MODE>(a, head);
   l.w = MODE == LM_SCALED && l.h.live ? a.wseq[l.h.b] : 0.0f;
@@ -53,12 +59,19 @@ __device__ __forceinline__ void lane_load(const RowArgs& a, LaneLoad<T, NE, VEC,
   if (l.blank) return;
   const T* x = row_at<T>(a.x, row, a.ldx);
   // past the row: -inf, whose exponential is 0 around any base of a row that has one
-  if (VEC) {
+  if (LAY) {
+    Split sp{0, a.V / VE, 0};
+    if (LAY == SPLIT) sp = split_row(x, a.V);
 #pragma unroll
     for (int i = 0; i < NE / VE; ++i) {
       constexpr uint32_t none = Vec<T>::LOWEST;
       l.x.q[i] = make_uint4(none, none, none, none);
-      if (Map::at(i * VE, lane) < a.V) l.x.q[i] = __ldg(reinterpret_cast<const uint4*>(x) + (i * L + lane));
+      if (i * L + lane < sp.nb)
+        l.x.q[i] = __ldg(reinterpret_cast<const uint4*>(x + sp.head) + (i * L + lane));
+    }
+    if (LAY == SPLIT) {
+      l.x.e[0] = from_f32<T>(NEG_INF);
+      if (lane < sp.edge) l.x.e[0] = x[edge_index<T>(sp, lane)];
     }
   } else {
 #pragma unroll
@@ -77,10 +90,10 @@ __device__ __forceinline__ void lane_load(const RowArgs& a, LaneLoad<T, NE, VEC,
 
 // One row.  KEEP: teacher's entries that a lane keeps in registers; 0: they go
 // through shared memory (lists of more than 128).
-template <typename T, int MODE, int L, int NE, bool VEC, int KEEP, int AHEAD>
-__device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, AHEAD>& now, int r,
+template <typename T, int MODE, int L, int NE, int LAY, int KEEP, int AHEAD>
+__device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, AHEAD>& now, int r,
                                          const Teacher& tc, int lane, unsigned mm) {
-  using Map = LaneMap<T, L, VEC>;
+  using Map = LaneMap<T, L, LAY>;
   constexpr int VE = vec_of<T>;
   constexpr bool SHORT = KEEP > 0;
   const int V = a.V;
@@ -123,8 +136,13 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, 
 
   f32x2 v[NE / 2];
   float top = NEG_INF;
-  if constexpr (VEC) {
+  float xe = NEG_INF;
+  if constexpr (LAY != ELEMENTS) {
     top = Vec<T>::greatest(now.x.q);
+    if (LAY == SPLIT) {
+      xe = to_f32<T>(now.x.e[0]);
+      top = fmaxf(top, xe);
+    }
 #pragma unroll
     for (int i = 0; i < NE / VE; ++i) {
       f32x2 two[VE / 2];
@@ -159,12 +177,14 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, 
       v[i] = pair(ex2((lo - base.at) * a.sl), ex2((hi - base.at) * a.sl));
     }
   }
+  if (LAY == SPLIT) xe = based_exp(xe, a.sl, base);
   if (MODE != LM_SCALED) {
     f32x2 part[2] = {v[0], v[1]};
 #pragma unroll
     for (int i = 2; i < NE / 2; ++i) part[i & 1] = add2(part[i & 1], v[i]);
     float lo, hi;
     halves(add2(part[0], part[1]), lo, hi);
+    if (LAY == SPLIT) lo += xe;
     S = lanes_sum(lo + hi, L, mm);
   }
 
@@ -195,11 +215,13 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, 
   const f32x2 scale2 = pair(scale, scale);
 #pragma unroll
   for (int i = 0; i < NE / 2; ++i) v[i] = mul2(v[i], scale2);
-  if constexpr (VEC) {
-    uint4* out = reinterpret_cast<uint4*>(g);
+  if constexpr (LAY != ELEMENTS) {
+    Split sp{0, V / VE, 0};
+    if (LAY == SPLIT) sp = split_row(x, V);
+    uint4* out = reinterpret_cast<uint4*>(g + sp.head);
 #pragma unroll
     for (int i = 0; i < NE / VE; ++i) {
-      if (Map::at(i * VE, lane) >= V) continue;
+      if (i * L + lane >= sp.nb) continue;
       f32x2 two[VE / 2];
 #pragma unroll
       for (int e = 0; e < VE / 2; ++e) two[e] = v[i * (VE / 2) + e];
@@ -210,6 +232,10 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, 
         for (int e = 0; e < VE / 2; ++e) two[e] = add2(two[e], old[e]);
       }
       out[i * L + lane] = Vec<T>::pack(two);
+    }
+    if (LAY == SPLIT && lane < sp.edge) {
+      const int at = edge_index<T>(sp, lane);
+      g[at] = from_f32<T>(xe * scale + (a.add ? to_f32<T>(g[at]) : 0.0f));
     }
   } else {
 #pragma unroll
@@ -297,7 +323,7 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, VEC, 
   }
 }
 
-template <typename T, int MODE, int L, int NE, bool VEC, int KEEP>
+template <typename T, int MODE, int L, int NE, int LAY, int KEEP>
 __global__ void __launch_bounds__(LANES_THREADS, lanes_ctas(NE))
     loss_lanes_kernel(const __grid_constant__ RowArgs a) {
   constexpr int AHEAD = KEEP ? KEEP : TEACHER_AHEAD;
@@ -312,12 +338,12 @@ __global__ void __launch_bounds__(LANES_THREADS, lanes_ctas(NE))
   float* mine = dyn + (size_t)(tid / L) * (MODE == LM_DISTILL ? words + teacher_table(a.k) : 0);
   const Teacher tc{mine, reinterpret_cast<int*>(mine + a.k), mine + 2 * a.k, mine + 3 * a.k,
                    reinterpret_cast<int*>(mine + words)};
-  LaneLoad<T, NE, VEC, AHEAD> row;
+  LaneLoad<T, NE, LAY, AHEAD> row;
   lane_load<T, MODE, L>(a, row, load_head<MODE>(a, r), r, lane);
-  lane_row<T, MODE, L, NE, VEC, KEEP>(a, row, r, tc, lane, mm);
+  lane_row<T, MODE, L, NE, LAY, KEEP>(a, row, r, tc, lane, mm);
 }
 
-template <typename T, int MODE, int L, int NE, bool VEC, int KEEP>
+template <typename T, int MODE, int L, int NE, int LAY, int KEEP>
 cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
   // 48 KB of shared memory for the teacher's entries: fewer rows a CTA where k is large
   int threads = LANES_THREADS;
@@ -329,36 +355,39 @@ cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
     smem = threads / L * row;
   }
   const long long rows = (long long)a.B * a.T, per = threads / L;
-  loss_lanes_kernel<T, MODE, L, NE, VEC, KEEP>
+  loss_lanes_kernel<T, MODE, L, NE, LAY, KEEP>
       <<<(unsigned)((rows + per - 1) / per), threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
 // NE: 8, 16 or (vectors only) 32 elements a lane.
-template <typename T, int MODE, int L, bool VEC, int KEEP>
+template <typename T, int MODE, int L, int LAY, int KEEP>
 cudaError_t launch_lanes_of(const RowArgs& a, cudaStream_t st) {
-  if (a.V <= 8 * L) return launch_lanes_shape<T, MODE, L, 8, VEC, KEEP>(a, st);
-  if (a.V <= 16 * L) return launch_lanes_shape<T, MODE, L, 16, VEC, KEEP>(a, st);
-  if constexpr (VEC && L < 32) return launch_lanes_shape<T, MODE, L, 32, VEC, KEEP>(a, st);
+  if (a.V <= 8 * L) return launch_lanes_shape<T, MODE, L, 8, LAY, KEEP>(a, st);
+  if (a.V <= 16 * L) return launch_lanes_shape<T, MODE, L, 16, LAY, KEEP>(a, st);
+  if constexpr (LAY != ELEMENTS && L < 32) return launch_lanes_shape<T, MODE, L, 32, LAY, KEEP>(a, st);
   if constexpr (L == 32) {
-    if (a.V <= 32 * L) return launch_lanes_shape<T, MODE, L, 32, VEC, KEEP>(a, st);
-    return launch_lanes_shape<T, MODE, L, 64, VEC, KEEP>(a, st);
+    if (a.V <= 32 * L) return launch_lanes_shape<T, MODE, L, 32, LAY, KEEP>(a, st);
+    return launch_lanes_shape<T, MODE, L, 64, LAY, KEEP>(a, st);
   }
   return cudaErrorInvalidValue;  // not reached: L is chosen by V
 }
 
-template <typename T, int MODE, bool VEC, int KEEP>
+template <typename T, int MODE, int LAY, int KEEP>
 cudaError_t launch_lanes_with(const RowArgs& a, int L, cudaStream_t st) {
-  if constexpr (KEEP != 4) {  // long lists come with L = 32
+  if constexpr (KEEP != 4 && LAY == SPLIT) {
+    if (L == 16) return launch_lanes_of<T, MODE, 16, LAY, KEEP>(a, st);
+  }
+  if constexpr (KEEP != 4 && LAY != SPLIT) {  // long lists come with L = 32, split rows with 16 or 32
     switch (L) {
-      case 1: return launch_lanes_of<T, MODE, 1, VEC, KEEP>(a, st);
-      case 2: return launch_lanes_of<T, MODE, 2, VEC, KEEP>(a, st);
-      case 4: return launch_lanes_of<T, MODE, 4, VEC, KEEP>(a, st);
-      case 8: return launch_lanes_of<T, MODE, 8, VEC, KEEP>(a, st);
-      case 16: return launch_lanes_of<T, MODE, 16, VEC, KEEP>(a, st);
+      case 1: return launch_lanes_of<T, MODE, 1, LAY, KEEP>(a, st);
+      case 2: return launch_lanes_of<T, MODE, 2, LAY, KEEP>(a, st);
+      case 4: return launch_lanes_of<T, MODE, 4, LAY, KEEP>(a, st);
+      case 8: return launch_lanes_of<T, MODE, 8, LAY, KEEP>(a, st);
+      case 16: return launch_lanes_of<T, MODE, 16, LAY, KEEP>(a, st);
     }
   }
-  return launch_lanes_of<T, MODE, 32, VEC, KEEP>(a, st);
+  return launch_lanes_of<T, MODE, 32, LAY, KEEP>(a, st);
 }
 
 // False where the row is too long for these kernels.
@@ -367,27 +396,35 @@ bool launch_lanes(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   if (a.V > LANES_V_MAX) return false;
   constexpr int VE = vec_of<T>;
   const bool grad = a.g != nullptr;
-  const bool vec = a.V % VE == 0 && a.ldx % VE == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
-                   (!grad || (a.ldg % VE == 0 && reinterpret_cast<uintptr_t>(a.g) % 16 == 0));
+  const uintptr_t px = reinterpret_cast<uintptr_t>(a.x), pg = reinterpret_cast<uintptr_t>(a.g);
+  const bool vec = a.V % VE == 0 && a.ldx % VE == 0 && px % 16 == 0 &&
+                   (!grad || (a.ldg % VE == 0 && pg % 16 == 0));
+  // gradient rows must share their scores' offset from a 16-byte boundary
+  const bool split = !vec && a.V > LANES_ELEMENTS &&
+                     (!grad || ((px ^ pg) % 16 == 0 && (a.ldx - a.ldg) % VE == 0));
   int L = 1;
   while (L < 32 && a.V > (vec ? 32 : 16) * L) L *= 2;
+  if (split) L = a.V <= 512 ? 16 : 32;  // a lane for each of up to 14 single elements
+  auto with = [&](auto keep, int lanes) {
+    constexpr int KEEP = decltype(keep)::value;
+    return vec ? launch_lanes_with<T, MODE, VECTORS, KEEP>(a, lanes, st)
+               : split ? launch_lanes_with<T, MODE, SPLIT, KEEP>(a, lanes, st)
+                       : launch_lanes_with<T, MODE, ELEMENTS, KEEP>(a, lanes, st);
+  };
   if constexpr (MODE == LM_DISTILL) {
     if (a.k <= 64) {
       while (a.k > 2 * L) L *= 2;
-      e = vec ? launch_lanes_with<T, MODE, true, 2>(a, L, st)
-              : launch_lanes_with<T, MODE, false, 2>(a, L, st);
+      e = with(std::integral_constant<int, 2>{}, L);
       return true;
     }
     if (a.k <= 128) {
-      e = vec ? launch_lanes_with<T, MODE, true, 4>(a, 32, st)
-              : launch_lanes_with<T, MODE, false, 4>(a, 32, st);
+      e = with(std::integral_constant<int, 4>{}, 32);
       return true;
     }
     // a lane holds its first entries in registers, and 48 KB hold a warp's rows
     const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float);
     while (L < 32 && (a.k > TEACHER_AHEAD * L || 32 / L * row > 48 * 1024)) L *= 2;
   }
-  e = vec ? launch_lanes_with<T, MODE, true, 0>(a, L, st)
-          : launch_lanes_with<T, MODE, false, 0>(a, L, st);
+  e = with(std::integral_constant<int, 0>{}, L);
   return true;
 }
