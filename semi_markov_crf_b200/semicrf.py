@@ -503,8 +503,10 @@ def _loss_grad(out, logits, grad, accumulate):
 
 
 def _loss_ws(ws, B, T, device):
-    if ws is None or ws.dims != (B, T):
+    if ws is None:
         return LossWorkspace(B, T, device)
+    if ws.dims != (B, T):  # a fresh one would leave the caller's status word stale
+        raise ValueError(f"ws is for (B, T) = {ws.dims}, not {(B, T)}")
     if ws.buf.device != device:
         raise TypeError(f"ws is on {ws.buf.device}, expected {device}")
     return ws

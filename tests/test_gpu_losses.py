@@ -18,6 +18,9 @@ Tolerances, from the arithmetic (u = 2^-24, half a step of float32).
 """
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -529,6 +532,253 @@ def test_runs_are_identical_and_captured_graphs_replay(V, dtype):
         torch.cuda.synchronize()
         for n in order:
             same(n, outs[n], want[n])
+
+
+@pytest.mark.parametrize("V", [9, 300, 1300, 5000, 70000])
+def test_single_positions(V):
+    """T = 1, the step that emits a label: the row pass writes the sequences'
+    sums itself, bad lengths and malformed labels included."""
+    from semi_markov_crf_b200 import semicrf
+    B, T = 7, 1
+    x, d = _logits(B, T, V, torch.bfloat16, V)
+    lens = [1, 1, 0, 1, 2, -1, 1]
+    lengths = torch.tensor(lens, dtype=torch.int32)
+    good = [v if v in (0, 1) else 0 for v in lens]
+    y = torch.randint(0, V, (B, T), generator=_gen(V), dtype=torch.int32)
+    y[3], y[6] = -1, V
+    ry = y.clone()
+    ry[6] = -1
+    old, reference = _policy_inputs(x, good, ry, 1.0, V)
+    adv = torch.randn(B, generator=_gen(1)).clamp(-2, 2)
+    want = ref.policy_loss(x, good, ry, old, adv, reference, 0.2, 0.3, 0.1)
+    for key in ("loss", "kl"):
+        want[key][[4, 5, 6]] = math.nan
+    want["logp"][6] = math.nan
+    ws = semicrf.LossWorkspace(B, T)
+    out = semicrf.policy_loss(d, lengths.cuda(), y.cuda(), old.cuda(), adv.cuda(),
+                              ref_logp=reference.cuda(), clip_high=0.3, kl_coef=0.1, ws=ws)
+    assert semicrf.get_status(ws) == 6
+    _policy_tolerances(out, want, good, V, 2.0, 0.1)
+    scale = (2 * (torch.nan_to_num(want["logp"]) - old.double()).exp() + 0.1) * (want["slope"] != 0)
+    _check_grad(out["grad_logits"], want["grad_logits"], scale, torch.bfloat16, V, 1.0, 2.0)
+    ids, teacher, _ = _teacher(x, 5, V)
+    out = semicrf.distill_loss(d, torch.ones(B, dtype=torch.int32).cuda(), ids.cuda(), teacher.cuda(),
+                               ws=ws)
+    assert semicrf.get_status(ws) == 0
+    want = ref.distill_loss(x, [1] * B, ids, teacher)
+    _check_distill(out, want, [1] * B, torch.bfloat16, V, 1.0)
+    out = semicrf.label_logprob(d, torch.ones(B, dtype=torch.int32).cuda(), ry.cuda(), ws=ws)
+    want = ref.label_logprob(x, [1] * B, ry)
+    _check("score", out["score"], want["score"], lse_tol(V) + 2 * U * want["score"].abs())
+
+
+@pytest.mark.parametrize("T", [2049, 9000, 70001])
+def test_long_sequences(T):
+    """Sums over sequences that one CTA does not cover: the kernels' own
+    per-position values added in float64 here (n u^2 of that sum is nothing:
+    one rounding of the float32 result, u, and one of each float32 term)."""
+    from semi_markov_crf_b200 import semicrf
+    B, V = 2, 5
+    x, d = _logits(B, T, V, torch.float32, T)
+    lens = [T, T - 700]
+    lengths = torch.tensor(lens, dtype=torch.int32).cuda()
+    y = torch.randint(0, V, (B, T), generator=_gen(T), dtype=torch.int32)
+    y[:, ::7] = -1
+    at = torch.arange(T)[None] < torch.tensor(lens)[:, None]
+    counts = (y >= 0) & at
+    logq = torch.log_softmax(x.double(), -1).gather(-1, y.clamp_min(0).long()[..., None])[..., 0]
+    logp = torch.where(counts, logq, torch.zeros_like(logq))
+    out = semicrf.label_logprob(d, lengths, y.cuda())
+    tol = (2 * U * logp.abs() + counts * lse_tol(V)).sum(1)
+    _check("score", out["score"], logp.sum(1), tol + U * logp.sum(1).abs())
+    reference = (logq + 0.1 * torch.randn(B, T, generator=_gen(2), dtype=torch.float64)).float()
+    for average in (False, True):
+        pairs = semicrf.preference_loss(d, lengths, y.cuda(), reference.cuda(), beta=0.01,
+                                        average=average)
+        n = counts.sum(1).double() if average else torch.ones(B, dtype=torch.float64)
+        ratio = torch.where(counts, logq - reference.double(), torch.zeros_like(logq))
+        want = 0.01 * ratio.sum(1) / n
+        e = 0.01 * counts.sum(1) * (lse_tol(V) + U) / n
+        _check("reward", pairs["reward"], want, e + U * want.abs())
+        slope = 0.01 * ref.preference_term(float(want[0] - want[1]), 0.0)[1]
+        q = torch.softmax(x.double(), -1)
+        base = torch.nn.functional.one_hot(y.clamp_min(0).long(), V).double() - q
+        sign = torch.tensor([slope, -slope], dtype=torch.float64) / n
+        grad = torch.where(counts[..., None], base * sign[:, None, None], torch.zeros_like(base))
+        # the weight's own error: 0.01 (d reward) on top of an entry's
+        _check("grad", pairs["grad_logits"], grad,
+               (sign.abs() * (3 * lse_tol(V) + 12 * U + 2 * float(e.max())))[:, None, None] + U * grad.abs())
+    old = (logq + 0.05).float()
+    pol = semicrf.policy_loss(d, lengths, y.cuda(), old.cuda(), torch.tensor([1.0, -1.0]).cuda(),
+                              ref_logp=reference.cuda(), kl_coef=0.1)
+    assert pol["clipped"].tolist() == [0, 0]  # exp(-0.05) is inside the clip
+    gap = torch.where(counts, reference.double() - logq, torch.zeros_like(logq))
+    kl = (torch.expm1(gap) - gap).sum(1)
+    _check("kl", pol["kl"], kl, counts.sum(1) * 2 * (lse_tol(V) + 4 * U) + U * kl)
+
+
+@pytest.mark.parametrize("V,dtype,k", [(8, torch.float32, 20), (300, torch.bfloat16, 100),
+                                       (1500, torch.float32, 129), (2048, torch.float16, 1024),
+                                       (3001, torch.float32, 1024), (262145, torch.float32, 30),
+                                       (600001, torch.float32, 40), (900001, torch.bfloat16, 3)])
+def test_distill_list_lengths(V, dtype, k):
+    """Lists of every length class at short, long and very wide rows (the last
+    two are wider than the rings of a cluster hold with a gradient), labels
+    repeated where the list is longer than a third of the vocabulary."""
+    from semi_markov_crf_b200 import semicrf
+    B, T = 2, 2
+    x, d = _logits(B, T, V, dtype, V)
+    ids = torch.randint(0, V, (B, T, k), generator=_gen(k), dtype=torch.int32)
+    ids[1, :, k // 2:] = -1
+    teacher = 2 * torch.randn(B, T, k, generator=_gen(k + 1))
+    want = ref.distill_loss(x, [2, 2], ids, teacher, None, 1.5)
+    out = semicrf.distill_loss(d, torch.tensor([2, 2], dtype=torch.int32).cuda(), ids.cuda(),
+                               teacher.cuda(), temperature=1.5)
+    _check_distill(out, want, [2, 2], dtype, V, 1.5)
+
+
+@pytest.mark.parametrize("V,dtype", [(600001, torch.float32), (900001, torch.bfloat16)])
+def test_very_wide_rows(V, dtype):
+    from semi_markov_crf_b200 import semicrf
+    B, T = 2, 2
+    x, d = _logits(B, T, V, dtype, V)
+    y = torch.randint(0, V, (B, T), generator=_gen(V), dtype=torch.int32)
+    lens = [2, 1]
+    lengths = torch.tensor(lens, dtype=torch.int32).cuda()
+    want = ref.label_logprob(x, lens, y, 0.9)
+    out = semicrf.label_logprob(d, lengths, y.cuda(), 0.9, grad=True)
+    _check("logp", out["logp"], want["logp"], lse_tol(V) + U * want["logp"].abs())
+    _check_grad(out["grad_logits"], want["grad_logits"], want["slope"], dtype, V, 0.9)
+    pairs = semicrf.preference_loss(d, lengths, y.cuda(), beta=0.1)
+    pref = ref.preference_loss(x, lens, y, beta=0.1)
+    _check_grad(pairs["grad_logits"], pref["grad_logits"], pref["slope"].abs() * (1 + T) + 1e-9, dtype, V,
+                1.0)
+
+
+@pytest.mark.parametrize("V", [6, 300, 1001, 5000, 140000])
+@pytest.mark.parametrize("pads", [(0, 5), (5, 0), (8, 8), (3, 7)])
+def test_gradient_rows_of_their_own_stride(V, pads):
+    """Scores and gradient with rows apart by different strides: what lies
+    between the gradient's rows stays as it was."""
+    from semi_markov_crf_b200 import semicrf
+    B, T = 3, 3
+    lens, lengths = [3, 0, 2], torch.tensor([3, 0, 2], dtype=torch.int32).cuda()
+    for dtype in (torch.float32, torch.bfloat16):
+        x, d = _logits(B, T, V, dtype, V, pads[0])
+        y = torch.randint(0, V, (B, T), generator=_gen(V), dtype=torch.int32)
+        ids, teacher, _ = _teacher(x, 6, V)
+        wide = torch.full((B, T, V + pads[1]), 7.0, dtype=dtype, device="cuda")
+        for name in ("label", "distill"):
+            wide.fill_(7.0)
+            out = {"grad_logits": wide[..., :V]}
+            if name == "label":
+                want = ref.label_logprob(x, lens, y)
+                semicrf.label_logprob(d, lengths, y.cuda(), grad=True, out=out)
+            else:
+                want = ref.distill_loss(x, lens, ids, teacher)
+                semicrf.distill_loss(d, lengths, ids.cuda(), teacher.cuda(), out=out)
+            _check_grad(out["grad_logits"], want["grad_logits"], want["slope"], dtype, V, 1.0, 2.0)
+            assert bool((wide[..., V:] == 7.0).all())
+
+
+def test_accumulate_over_a_cluster():
+    """A float32 row shared by a cluster, its gradient added to."""
+    from semi_markov_crf_b200 import semicrf
+    B, T, V = 2, 2, 131075
+    x, d = _logits(B, T, V, torch.float32, 3)
+    lengths = torch.tensor([2, 1], dtype=torch.int32).cuda()
+    ids, teacher, _ = _teacher(x, 50, 4, ragged=False)
+    plain = semicrf.distill_loss(d, lengths, ids.cuda(), teacher.cuda())["grad_logits"]
+    start = torch.randn(B, T, V, generator=_gen(2)).cuda()
+    added = semicrf.distill_loss(d, lengths, ids.cuda(), teacher.cuda(), accumulate=True,
+                                 out={"grad_logits": start.clone()})["grad_logits"]
+    tol = 2 * U * (start.abs() + plain.abs()) + 4 * U * plain.abs().amax(-1, keepdim=True)
+    assert bool(((added - (start + plain)).abs() <= tol).all())
+    assert torch.equal(added[1, 1], start[1, 1])
+
+
+def test_two_streams_at_once():
+    """Calls of two streams, each with its workspace, while the other runs."""
+    from semi_markov_crf_b200 import semicrf
+    sizes = [(33000, torch.bfloat16), (70000, torch.float32), (300, torch.float32)]
+    made = [_calls(V, dtype, seed=i, B=6, T=30) for i, (V, dtype) in enumerate(sizes)]
+    want = [{n: call() for n, call in calls.items()} for _, calls in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[] for _ in made]
+    for _ in range(3):
+        for i, (_, calls) in enumerate(made):
+            with torch.cuda.stream(streams[i]):
+                got[i].append({n: call() for n, call in calls.items()})
+    torch.cuda.synchronize()
+    for i, runs in enumerate(got):
+        for run in runs:
+            for n, o in run.items():
+                for k, v in o.items():
+                    assert torch.equal(torch.nan_to_num(v.float()),
+                                       torch.nan_to_num(want[i][n][k].float())), (sizes[i], n, k)
+
+
+def test_refused_calls_leave_the_outputs_alone():
+    from semi_markov_crf_b200 import semicrf
+    B, T, V = 2, 3, 40
+    d = torch.zeros(B, T, V, device="cuda")
+    lengths = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    y = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+    g = torch.full((B, T, V), 5.0, device="cuda")
+    cases = [
+        (semicrf.SemiCRFError, dict(temperature=0.0)),
+        (TypeError, dict(labels=y.long())),
+        (TypeError, dict(labels=y[:, :2].contiguous())),
+        (TypeError, dict(logits=d.transpose(1, 2))),
+        (TypeError, dict(out={"grad_logits": g.bfloat16()})),
+        (TypeError, dict(out={"grad_logits": g, "logp": torch.zeros(B, T + 1, device="cuda")})),
+        (semicrf.SemiCRFError, dict(out={"grad_logits": d})),       # in place
+        (ValueError, dict(ws=semicrf.LossWorkspace(B, T + 1))),
+        (ValueError, dict(accumulate=True, out={})),
+        (semicrf.SemiCRFError, dict(logits=d.bfloat16(), accumulate=True,
+                                    out={"grad_logits": g.bfloat16()})),
+    ]
+    for error, change in cases:
+        kw = dict(logits=d, lengths=lengths, labels=y, grad=True, out={"grad_logits": g})
+        kw.update(change)
+        with pytest.raises(error):
+            semicrf.label_logprob(**kw)
+    with pytest.raises(semicrf.SemiCRFError):
+        semicrf.preference_loss(d[:1], lengths[:1], y[:1])
+    assert bool((g == 5.0).all()) and bool((d == 0.0).all())
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first call of each kind is captured (nothing may be
+    allocated or synchronised in there)."""
+    code = """
+import sys; sys.path[:0] = [%r, %r]
+import torch
+from semi_markov_crf_b200 import semicrf
+for V in (50, 1500, 20000, 140000):
+    B, T = 4, 3
+    d = torch.randn(B, T, V, device="cuda")
+    lengths = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    y = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+    ws = semicrf.LossWorkspace(B, T)
+    out = {k: torch.zeros(s, device="cuda") for k, s in
+           (("loss", (B // 2,)), ("reward", (B,)), ("logp", (B, T)), ("grad_logits", (B, T, V)))}
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        semicrf.preference_loss(d, lengths, y, ws=ws, out=out)
+    g.replay()
+    torch.cuda.synchronize()
+    want = semicrf.preference_loss(d, lengths, y)
+    assert torch.equal(want["grad_logits"], out["grad_logits"]), V
+    assert semicrf.get_status(ws) == 0
+print("captured")
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    res = subprocess.run([sys.executable, "-c", code % (os.path.dirname(here), here)],
+                         capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "captured" in res.stdout, res.stderr[-2000:]
 
 
 def test_rows_beyond_32_bit_offsets():
