@@ -195,11 +195,11 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
   } else if (MODE == LM_DISTILL) {
     P = th.P;
     if constexpr (SHORT) {
-      const float log2S = log2f(S);
+      const TeacherGap gap = teacher_gap(a, th, base, S);
       float part = 0.0f;
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u)
-        tp[u] = now.ahead.id[u] >= 0 ? teacher_p(a, th, base, log2S, now.ahead.t[u], tx[u], part) : 0.0f;
+        tp[u] = now.ahead.id[u] >= 0 ? teacher_p(a, th, gap, now.ahead.t[u], tx[u], part) : 0.0f;
       part = lanes_sum(part, L, mm);
       if (lane == 0) put_term(a, r, (float)(a.tau * a.tau) * part);
     } else {

@@ -71,6 +71,15 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// This warp is done with a chunk.  Its reads are ordinary accesses and the copy
+// that follows is an asynchronous one: without the fence between the two the
+// copy may overtake reads that are still under way.
+__device__ __forceinline__ void give_back(uint64_t* empty, int lane) {
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(empty);
+}
+
 // A position in a group's ring.
 struct Cursor {
   int slot;
@@ -287,11 +296,6 @@ __device__ __forceinline__ void ring_reduce(const RowArgs& a, const RingPlace& p
       uint4 raw[RING_NV];
       take_chunk<T>(raw, reinterpret_cast<const uint4*>(pl.ring + (size_t)cur.slot * pl.chunk_bytes),
                     gt, GT, n - c);
-      if (RELEASE) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&st.empty[cur.slot]);
-      }
-      cur.next(pl.slots);
       const float nb = fmaxf(mb, Vec<T>::greatest(raw) * a.sl);
       const float at = nb == NEG_INF ? 0.0f : nb;  // nothing above -inf yet: exponentials of 0
       const f32x2 at2 = pair(-at, -at);
@@ -306,6 +310,8 @@ __device__ __forceinline__ void ring_reduce(const RowArgs& a, const RingPlace& p
       }
       float sum, odd;
       halves(add2(sum2[0], sum2[1]), sum, odd);
+      if (RELEASE) give_back(&st.empty[cur.slot], lane);
+      cur.next(pl.slots);
       s = (mb == NEG_INF && s == 0.0f ? 0.0f : s * ex2(mb - nb)) + (sum + odd);
       mb = nb;
     }
@@ -360,8 +366,6 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
         if (plain) {
           uint4 raw[RING_NV];
           take_chunk<T>(raw, chunk, gt, GT, have);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&st.empty[cur.slot]);
 #pragma unroll
           for (int i = 0; i < RING_NV; ++i) {
             f32x2 v[Vec<T>::PAIRS];
@@ -371,6 +375,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
               v[e] = mul2(ex2_of_pair<T>(fma2(v[e], sl2, at2), e), scale2);
             raw[i] = Vec<T>::pack(v);
           }
+          give_back(&st.empty[cur.slot], lane);
           uint4* out = reinterpret_cast<uint4*>(gb) + c + gt;
           if (have >= chunk_vecs) {
 #pragma unroll
@@ -396,8 +401,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
               to[e] = from_f32<T>(gv);
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&st.empty[cur.slot]);
+          give_back(&st.empty[cur.slot], lane);
         }
         cur.next(pl.slots);
       }

@@ -260,7 +260,8 @@ __host__ __device__ inline int teacher_table(int k) {
 }
 
 struct TeacherHead {
-  float tm, tlog, P;
+  float tm, pT, P;
+  double tlog;
   bool malformed;
   bool repeats;  // two entries may have the same label
 };
@@ -298,27 +299,43 @@ struct TeacherLoad {
 };
 using TeacherAhead = TeacherLoad<TEACHER_AHEAD>;
 
-// log-sum-exp and total probability of a teacher whose greatest logit is tm
-// and whose exponentials around it sum to s.
+// Total probability of a teacher whose greatest logit is tm and whose
+// exponentials around it sum to s: an entry's probability is its exponential
+// times pT.
 __device__ __forceinline__ void teacher_total(const RowArgs& a, float lse, float s, TeacherHead& th) {
   if (a.tlse) {
-    th.tlog = (float)((double)lse - (double)th.tm * a.s);
-    th.P = s * expf(-th.tlog);
+    th.tlog = (double)lse - (double)th.tm * a.s;
+    const float hi = (float)th.tlog;
+    th.pT = expf(-hi) * (1.0f - (float)(th.tlog - (double)hi));
+    th.P = s * th.pT;
   } else {
-    th.tlog = logf(s);
+    th.tlog = log_of_sum(s);
+    th.pT = 1.0f / s;
     th.P = s > 0.0f ? 1.0f : s;  // no entry with a probability: no loss, no gradient
   }
 }
 
-// An entry's probability and its term of the loss, log p - log q taken from
-// differences with both maxima.
-__device__ __forceinline__ float teacher_p(const RowArgs& a, const TeacherHead& th, const Base& h,
-                                           float log2S, float t, float x, float& part) {
+// log p - log q of an entry with logit t and score x is ((t - tm) - (x - xm))
+// / temperature + c: the two maxima and logarithms of sums are taken apart in
+// float64 once a row, and what is left to float32 are small differences.
+struct TeacherGap {
+  float xm, c;
+};
+__device__ __forceinline__ TeacherGap teacher_gap(const RowArgs& a, const TeacherHead& th, const Base& h,
+                                                  float S) {
+  const double m = base_score(h, a.inv_sl);
+  TeacherGap g;
+  g.xm = (float)m;
+  g.c = (float)(log_of_sum(S) - th.tlog - ((double)g.xm - m) * a.s);
+  return g;
+}
+
+// An entry's probability; its term of the loss goes to `part`.
+__device__ __forceinline__ float teacher_p(const RowArgs& a, const TeacherHead& th, const TeacherGap& g,
+                                           float t, float x, float& part) {
   if (t == NEG_INF) return 0.0f;
-  const float lt = fmaf(t - th.tm, (float)a.s, -th.tlog);
-  const float p = expf(lt);
-  const float lq = (h.direct ? fmaf(x, a.sl, -h.at) : (x - h.at) * a.sl) - log2S;
-  if (p != 0.0f) part += p * fmaf(lq, -(float)LN2_D, lt);
+  const float dt = t - th.tm, p = expf(dt * (float)a.s) * th.pT;
+  if (p != 0.0f) part += p * fmaf(dt - (x - g.xm), (float)a.s, g.c);
   return p;
 }
 
@@ -387,10 +404,10 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
 __device__ __forceinline__ void teacher_terms(const RowArgs& a, long long r, const Teacher& tc,
                                               const TeacherHead& th, const Base& h, float S,
                                               bool loss, int lane, int n, unsigned mm) {
-  const float log2S = log2f(S);
+  const TeacherGap gap = teacher_gap(a, th, h, S);
   float part = 0.0f;
   for (int j = lane; j < a.k; j += n)
-    tc.p[j] = tc.id[j] >= 0 ? teacher_p(a, th, h, log2S, tc.p[j], tc.x[j], part) : 0.0f;
+    tc.p[j] = tc.id[j] >= 0 ? teacher_p(a, th, gap, tc.p[j], tc.x[j], part) : 0.0f;
   __syncwarp(mm);
   if (loss) {
     part = lanes_sum(part, n, mm);

@@ -781,6 +781,72 @@ print("captured")
     assert res.returncode == 0 and "captured" in res.stdout, res.stderr[-2000:]
 
 
+@pytest.mark.parametrize("op,rows,V,dtype", [
+    ("distill", 1500, 100003, torch.float32), ("policy", 1500, 100003, torch.float32),
+    ("logprob", 3000, 65537, torch.bfloat16), ("preference", 3000, 40001, torch.float32),
+    ("policy", 4000, 30000, torch.float16), ("distill", 6000, 6000, torch.bfloat16),
+    ("logprob", 40000, 1001, torch.float32)])
+def test_streamed_rows_are_whole_and_the_same_every_time(op, rows, V, dtype):
+    """Many rows through every ring: a chunk given back before its last reader
+    has it mixes rows.  Each gradient row against an elementary float32 form of
+    it (errors of that form: as the kernel's), and 12 runs bit for bit.  The
+    form takes its factor a from float32 outputs: a ratio from logp, u |logp|
+    relative and 12 u for the sum and the exponential; the pair's slope from
+    two rewards, each rounded by u |reward|, and the logistic's slope changes by
+    at most its own value per unit."""
+    from semi_markov_crf_b200 import semicrf
+    B, T = 2, rows // 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    d = torch.empty(B, T, V, dtype=dtype, device="cuda")
+    d.normal_(generator=g).mul_(2)
+    lengths = torch.tensor([T, T - 5], dtype=torch.int32).cuda()
+    y = torch.randint(0, V, (B, T), generator=g, device="cuda", dtype=torch.int32)
+    old = torch.full((B, T), -8.0, device="cuda")
+    adv = torch.tensor([0.5, -0.5]).cuda()
+    ids = torch.argsort(torch.rand(B, T, 90, generator=g, device="cuda"), -1).int() * (V // 100)
+    teacher = torch.randn(B, T, 90, generator=g, device="cuda")
+    w = torch.ones(B, dtype=torch.float64, device="cuda")
+    call = {"logprob": lambda: semicrf.label_logprob(d, lengths, y, grad=True),
+            "policy": lambda: semicrf.policy_loss(d, lengths, y, old, adv),
+            "preference": lambda: semicrf.preference_loss(d, lengths, y, beta=0.001),
+            "distill": lambda: semicrf.distill_loss(d, lengths, ids, teacher, grad_loss=w)}[op]
+    first = {k: v.clone() for k, v in call().items()}
+    for _ in range(12):
+        for k, v in call().items():
+            assert torch.equal(v, first[k]), k
+    logp = semicrf.label_logprob(d, lengths, y)["logp"]
+    if op == "preference":
+        slope = 0.001 * ref.preference_term(float(first["reward"][0] - first["reward"][1]), 0.0)[1]
+    for b in range(B):
+        for t0 in range(0, T, 250):
+            at = slice(t0, min(t0 + 250, T))
+            q = torch.softmax(d[b, at].float(), -1)
+            n = q.shape[0]
+            live = (torch.arange(t0, t0 + n, device="cuda") < lengths[b])[:, None]
+            if op == "distill":
+                p = torch.softmax(teacher[b, at], -1)
+                want = q.scatter_add(1, ids[b, at].long(), -p)
+                a = torch.ones(n, 1, device="cuda")
+            else:
+                hot = torch.zeros_like(q).scatter_(1, y[b, at].long()[:, None], 1.0)
+                a = torch.ones(n, 1, device="cuda")
+                if op == "preference":
+                    a = a * (slope if b == 0 else -slope)
+                if op == "policy":
+                    r = (logp[b, at] + 8.0).exp()[:, None]
+                    held = (r > 1.2) if b == 0 else (r < 0.8)
+                    a = torch.where(held, torch.zeros_like(r), -adv[b] * r)
+                want = a * (hot - q)
+            want = torch.where(live, want, torch.zeros_like(want))
+            own = (U * (logp[b, at].abs()[:, None] + 12) if op == "policy" else
+                   U * (2 * float(first["reward"].abs().max()) + 12) if op == "preference" else 0.0)
+            tol = a.abs() * (q * (8 * lse_tol(V) + 40 * U) + 2e-7 + own) + HALF[dtype] * want.abs() \
+                + TINY[dtype]
+            err = (first["grad_logits"][b, at].float() - want).abs()
+            assert bool((err <= tol + 1e-30).all()), (b, t0, float((err - tol).max()))
+
+
 def test_rows_beyond_32_bit_offsets():
     """More than 2^31 scores: the last rows against the same rows alone."""
     from semi_markov_crf_b200 import semicrf
