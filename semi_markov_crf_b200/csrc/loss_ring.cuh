@@ -748,7 +748,7 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   s.W = 2;
   while (s.W < RING_WARPS &&
          (row > (size_t)s.W * 8 * 1024 || rows <= (long long)sms * (RING_WARPS / s.W) / 2 ||
-          RING_WARPS / s.W * entry > 40 * 1024))
+          RING_WARPS / s.W * entry > 64 * 1024))
     s.W *= 2;
   size_t chunk, fixed;
   for (;; s.W *= 2) {

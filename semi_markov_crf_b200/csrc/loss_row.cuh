@@ -638,6 +638,7 @@ __device__ __forceinline__ int edge_index(const Split& s, int i) {
 }
 
 #include "loss_lanes.cuh"
+#include "loss_cta.cuh"
 #include "loss_ring.cuh"
 #include "loss_wide.cuh"
 
@@ -646,6 +647,7 @@ template <typename T, int MODE>
 cudaError_t rows_in_mode(const RowArgs& a, cudaStream_t st) {
   cudaError_t e;
   if (launch_lanes<T, MODE>(a, st, e)) return e;
+  if (launch_cta<T, MODE>(a, st, e)) return e;
   if (launch_ring<T, MODE>(a, st, e)) return e;
   return launch_wide<T, MODE>(a, st);
 }
