@@ -68,8 +68,6 @@ __global__ void __launch_bounds__(L, 640 / L)
   float xe = NEG_INF;
   if (ei >= 0) xe = to_f32<T>(x[ei]);
   const LabelIn<T> in = load_label<T, MODE>(a, r, h, x);
-  float2 stat{};
-  if (MODE == LM_SCALED) stat = a.stat[r];
   const Range all{0, V, V};
   const Teacher tc{dyn, reinterpret_cast<int*>(dyn + a.k), dyn + 2 * a.k, dyn + 3 * a.k,
                    reinterpret_cast<int*>(dyn + TEACHER_WORDS * a.k)};
@@ -77,7 +75,7 @@ __global__ void __launch_bounds__(L, 640 / L)
   if (MODE == LM_DISTILL && warp == 0) {
     TeacherAhead ahead;
     ahead.load(a, r, 0, lane, 32);
-    th = teacher_head<T>(a, r, tc, ahead, x, g, all, lane, 32, FULL_MASK);
+    th = teacher_head<T>(a, r, in.lse, tc, ahead, x, g, all, lane, 32, FULL_MASK);
     if (lane == 0) {
       tshare[0] = th.P;
       tshare[1] = th.malformed ? 1.0f : 0.0f;
@@ -86,7 +84,7 @@ __global__ void __launch_bounds__(L, 640 / L)
 
   Base base;
   float S = 0.0f;
-  if (MODE == LM_SCALED) base = unpack_stat(stat, S);
+  if (MODE == LM_SCALED) base = unpack_stat(in.stat, S);
   else base = make_base(cta_max<L>(fmaxf(Vec<T>::greatest(q), xe), red[0]), a.sl);
   if (MODE == LM_DISTILL && tshare[1] != 0.0f) {
     if (tid == 0) blank_outputs<MODE>(a, r, true);
@@ -130,7 +128,7 @@ __global__ void __launch_bounds__(L, 640 / L)
   } else if (MODE == LM_DISTILL) {
     P = tshare[0];
     if (warp == 0) teacher_terms(a, r, tc, th, base, S, true, lane, 32, FULL_MASK);
-    cq = (float)((a.w ? a.w[h.b] : 1.0) * a.tau);
+    cq = (float)(in.w * a.tau);
   } else {
     cy = label_outputs<MODE>(a, r, in, base, S, tid == 0);
     cq = -cy;

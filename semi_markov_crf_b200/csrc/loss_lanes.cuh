@@ -81,10 +81,9 @@ __device__ __forceinline__ void lane_load(const RowArgs& a, LaneLoad<T, NE, LAY,
     }
   }
   if (MODE == LM_SCALED) l.stat = a.stat[row];
-  if (has_label(MODE) && MODE != LM_SCALED) l.in = load_label<T, MODE>(a, row, l.h, x);
+  if (MODE != LM_SCALED) l.in = load_label<T, MODE>(a, row, l.h, x);
   if (MODE == LM_DISTILL) {
     l.ahead.load(a, row, 0, lane, L);
-    l.in.w = a.w ? a.w[l.h.b] : 1.0;
   }
 }
 
@@ -121,9 +120,9 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u)
         if (now.ahead.id[u] >= 0) s += expf((now.ahead.t[u] - th.tm) * (float)a.s);
-      teacher_total(a, a.tlse ? a.tlse[r] : 0.0f, lanes_sum(s, L, mm), th);
+      teacher_total(a, now.in.lse, lanes_sum(s, L, mm), th);
     } else {
-      th = teacher_head<T>(a, r, tc, now.ahead, x, g, all, lane, L, mm);
+      th = teacher_head<T>(a, r, now.in.lse, tc, now.ahead, x, g, all, lane, L, mm);
     }
     blank = malformed = th.malformed;
   }

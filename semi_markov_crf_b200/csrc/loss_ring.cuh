@@ -478,7 +478,7 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
       TeacherHead th{};
       if (MODE == LM_DISTILL) {
         if (ahead_row != r) ahead.load(a, r, 0, lane, 32);
-        th = teacher_head<T>(a, r, tc, ahead, x, g, rg, lane, 32, FULL_MASK);
+        th = teacher_head<T>(a, r, in.lse, tc, ahead, x, g, rg, lane, 32, FULL_MASK);
         ahead_row = r + pl.units;
         if (ahead_row < pl.rows) ahead.load(a, ahead_row, 0, lane, 32);
       }
@@ -536,7 +536,7 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
           base.at = m;
         }
       } else {
-        base = unpack_stat(a.stat[r], S);
+        base = unpack_stat(in.stat, S);
       }
 
       float cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
@@ -547,7 +547,7 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
       } else if (MODE == LM_DISTILL) {
         P = th.P;
         zero = th.malformed;
-        cq = (float)((a.w ? a.w[h.b] : 1.0) * a.tau);
+        cq = (float)(in.w * a.tau);
       } else {
         cy = label_outputs<MODE>(a, r, in, base, S, lane == 0 && pl.rank == 0);
         cq = -cy;

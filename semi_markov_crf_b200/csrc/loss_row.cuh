@@ -151,6 +151,8 @@ template <typename T>
 struct LabelIn {
   T score;  // of the label, as loaded: converting it would wait for it
   float slope, old_logp, ref_logp, adv;
+  float lse;    // LM_DISTILL: the teacher's
+  float2 stat;  // LM_SCALED
   double w;
   __device__ float xy() const { return to_f32<T>(score); }
 };
@@ -160,6 +162,9 @@ __device__ __forceinline__ LabelIn<T> load_label(const RowArgs& a, long long r, 
                                               const T* x) {
   LabelIn<T> in{};
   in.w = 1.0;
+  if (a.w) in.w = a.w[h.b];
+  if (MODE == LM_DISTILL && a.tlse) in.lse = a.tlse[r];
+  if (MODE == LM_SCALED) in.stat = a.stat[r];
   if (!has_label(MODE)) return in;
   in.score = x[h.y];
   if (MODE == LM_LOGPROB) in.slope = a.grad_logp ? a.grad_logp[r] : 1.0f;
@@ -168,7 +173,6 @@ __device__ __forceinline__ LabelIn<T> load_label(const RowArgs& a, long long r, 
     in.old_logp = a.old_logp[r];
     in.adv = a.adv[a.adv_tok ? r : (long long)h.b];
   }
-  if (a.w) in.w = a.w[h.b];
   return in;
 }
 
@@ -342,8 +346,8 @@ __device__ __forceinline__ float teacher_p(const RowArgs& a, const TeacherHead& 
 // Takes the entries in (the first ones are in `ahead`); the maximum and
 // log-sum-exp of the teacher's logits over those in use.
 template <typename T>
-__device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long r, const Teacher& tc,
-                                                    TeacherAhead& ahead, const T* x, const T* g,
+__device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long r, float lse,
+                                                    const Teacher& tc, TeacherAhead& ahead, const T* x, const T* g,
                                                     const Range& rg, int lane, int n, unsigned mm) {
   TeacherHead th;
   const float st = (float)a.s;
@@ -375,10 +379,11 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
   m = lanes_max(m, n, mm);
   th.tm = m == NEG_INF ? 0.0f : m;
   float s = 0.0f;
+#pragma unroll 4
   for (int j = lane; j < a.k; j += n)
     if (tc.id[j] >= 0) s += expf((tc.p[j] - th.tm) * st);
   s = lanes_sum(s, n, mm);
-  teacher_total(a, a.tlse ? a.tlse[r] : 0.0f, s, th);
+  teacher_total(a, lse, s, th);
   th.repeats = true;
   const int size = teacher_table(a.k);
   if (size) {
@@ -406,6 +411,7 @@ __device__ __forceinline__ void teacher_terms(const RowArgs& a, long long r, con
                                               bool loss, int lane, int n, unsigned mm) {
   const TeacherGap gap = teacher_gap(a, th, h, S);
   float part = 0.0f;
+#pragma unroll 4
   for (int j = lane; j < a.k; j += n)
     tc.p[j] = tc.id[j] >= 0 ? teacher_p(a, th, gap, tc.p[j], tc.x[j], part) : 0.0f;
   __syncwarp(mm);
@@ -422,6 +428,7 @@ template <typename T>
 __device__ __forceinline__ void teacher_fix(const RowArgs& a, const Teacher& tc, T* g,
                                             const Base& h, float scale, float cq, bool repeats,
                                             int lane, int n, const Range& rg) {
+#pragma unroll 4
   for (int j = lane; j < a.k; j += n) {
     const int id = tc.id[j];
     if (id < 0 || !rg.has(id)) continue;

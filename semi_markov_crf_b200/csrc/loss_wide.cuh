@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
     if (warp == 0) {
       TeacherAhead ahead;
       ahead.load(a, r, 0, lane, 32);
-      th = teacher_head<T>(a, r, tc, ahead, x, g, all, lane, 32, FULL_MASK);
+      th = teacher_head<T>(a, r, a.tlse ? a.tlse[r] : 0.0f, tc, ahead, x, g, all, lane, 32, FULL_MASK);
       if (lane == 0) {
         tshare[0] = th.P;
         tshare[1] = th.malformed ? 1.0f : 0.0f;
