@@ -8,7 +8,7 @@
 // shuffles, one row a group, and no more registers than 28 to 40 warps an SM
 // leave.  (Loading a row ahead costs the registers of a third of the warps
 // and was slower: 31 against 21 us for 80000 rows of 128 float32; tiles in
-// shared memory behind TMA copies, 16 warps an SM, took 28.)
+// shared memory behind TMA copies, 16 warps an SM, took 33.)
 //
 // Layouts: VECTORS, rows on 16-byte boundaries; SPLIT, the 16-byte vectors
 // within a row and up to 14 single elements, one a lane; ELEMENTS, neighbouring

@@ -11,10 +11,13 @@
 //
 // A position costs one read of its V scores, and one write of V gradient
 // entries: bytes bound it (about five float32 operations and one exponential
-// an element).  Sums of exponentials are float32 relative to the running
-// maximum, which is kept in the scores' own units so that rows masked with
-// the type's lowest value still have a softmax; what follows from them for a
-// position (logp, the ratio, the loss) is float64 or exact differences.
+// an element).  Sums of exponentials are float32 around the row's maximum;
+// what follows from them for a position (logp, the ratio, the loss) is float64
+// or small differences, rounded once.
+//
+// By length of the row: loss_lanes.cuh (to 2048 scores, lane groups),
+// loss_cta.cuh (to 8192, a CTA a row), loss_ring.cuh (persistent CTAs and
+// clusters), loss_wide.cuh (what a cluster does not hold).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -24,10 +27,6 @@
 #include <atomic>
 
 #include "loss.cuh"
-
-#ifndef LOSS_POLY
-#define LOSS_POLY 9
-#endif
 
 namespace semicrf {
 
@@ -483,40 +482,6 @@ __device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
   float lo, hi;
   halves(v, lo, hi);
   return pair(ex2(lo), ex2(hi));
-}
-
-// 2^t for t <= 0 on the FMA pipe, beside the special-function unit's ex2 (16 a
-// clock and SM): t is split into its nearest integer n and f in [-1/2, 1/2]
-// (Cody and Waite), 2^f is the degree-5 polynomial of least relative error
-// there (Remez exchange; 2e-7 with its coefficients and steps in float32, as
-// ex2.approx), and 2^n is put together from its exponent.  Below -127 the
-// result is 0 exactly; a NaN stays one.
-__device__ __forceinline__ f32x2 ex2_2_poly(f32x2 t) {
-  float lo, hi;
-  halves(t, lo, hi);
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(-127.0f));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(-127.0f));
-  t = pair(lo, hi);
-  constexpr float round = 12582912.0f;  // 1.5 * 2^23: adding it leaves the nearest integer
-  const f32x2 n = add2(t, pair(round, round));
-  const f32x2 f = add2(t, mul2(add2(n, pair(-round, -round)), pair(-1.0f, -1.0f)));
-  f32x2 p = pair(0.0013276472f, 0.0013276472f);
-  p = fma2(p, f, pair(0.009675541f, 0.009675541f));
-  p = fma2(p, f, pair(0.05550713f, 0.05550713f));
-  p = fma2(p, f, pair(0.2402212f, 0.2402212f));
-  p = fma2(p, f, pair(0.69314694f, 0.69314694f));
-  p = fma2(p, f, pair(1.0000001f, 1.0000001f));
-  halves(n, lo, hi);
-  const float el = __int_as_float((__float_as_int(lo) << 23) + 0x3f800000);
-  const float eh = __int_as_float((__float_as_int(hi) << 23) + 0x3f800000);
-  return mul2(p, pair(el, eh));
-}
-
-// Exponentials of pair e of a vector: of the 16-bit types, whose elements are
-// cheap to move, every fourth pair takes the FMA pipe.
-template <typename T>
-__device__ __forceinline__ f32x2 ex2_of_pair(f32x2 v, int e) {
-  return sizeof(T) == 2 && e == LOSS_POLY ? ex2_2_poly(v) : ex2_2(v);
 }
 
 // A 16-byte vector of T as pairs of float32, its greatest element, -inf, and back.
