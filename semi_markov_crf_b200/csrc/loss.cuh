@@ -49,7 +49,8 @@ struct RowArgs {
   uint8_t* clip;           // [B, T] LM_POLICY
   float2* stat;            // [B, T] LM_PREFERENCE: a row's base and sum of exponentials
   float* wseq;             // [B] LM_SCALED: d loss / d logp of the sequence's positions
-  int* status;             // cleared by the pass (nullptr: left alone)
+  int* status;             // cleared by the pass, unless
+  int keep_status;         // it follows another one of the same call
   // One position a sequence (T = 1): the pass writes the sequences' sums itself.
   int single;
   float* seq_sum;          // [B] each nullable

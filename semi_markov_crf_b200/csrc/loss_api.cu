@@ -91,7 +91,7 @@ int prepare_rows(const void* logits, int dtype, int64_t ld, const int32_t* lengt
 
 int run_rows(int mode, int dtype, const RowArgs& a, cudaStream_t st) {
   if (a.T == 0)  // no rows: the pass that clears the status word does not run
-    return !a.status || cudaMemsetAsync(a.status, 0, sizeof(int), st) == cudaSuccess
+    return a.keep_status || cudaMemsetAsync(a.status, 0, sizeof(int), st) == cudaSuccess
                ? SEMICRF_OK
                : SEMICRF_ERR_CUDA;
   LaunchTimer lt("loss_rows_kernel", st);
@@ -262,7 +262,7 @@ extern "C" int semicrf_preference_loss(const void* logits, int dtype, int64_t ld
     if (launch_loss_pairs(q, st) != cudaSuccess) return SEMICRF_ERR_CUDA;
   }
   if (!grad_logits) return SEMICRF_OK;
-  a.status = nullptr;
+  a.keep_status = 1;
   return run_rows(LM_SCALED, dtype, a, st);
 }
 

@@ -278,7 +278,7 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
       for (int u = 0; u < AHEAD; ++u) {
         const int id = now.ahead.id[u];
         if (id < 0) continue;
-        for (unsigned at = (unsigned)id * 2654435769u;; ++at) {
+        for (unsigned at = teacher_slot(id, size);; ++at) {
           const int was = atomicCAS(&tc.table[at & (size - 1)], -1, id);
           if (was == id) twice = 1.0f;
           if (was == -1 || was == id) break;
@@ -409,7 +409,7 @@ bool launch_lanes(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   // elements a lane; 16-bit rows that are only read leave registers for more
   // (262144 rows of 1000: 116 against 130 us)
   const int most = !vec ? 16 : grad || ES == 4 ? 32 : 64;
-  while (L < 32 && a.V > (L == 1 ? 32 : most) * L) L *= 2;
+  while (L < 32 && a.V > (L == 1 ? std::min(32, most) : most) * L) L *= 2;
   if (split) L = a.V <= (grad || ES == 4 ? 512 : 1024) ? 16 : 32;  // a lane for each of up to 14 single elements
   auto with = [&](auto keep, int lanes) {
     constexpr int KEEP = decltype(keep)::value;

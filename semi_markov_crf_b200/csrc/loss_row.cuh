@@ -179,7 +179,7 @@ __device__ __forceinline__ LabelIn<T> load_label(const RowArgs& a, long long r, 
 // is no pass over the sequences that would look at the lengths, so the first
 // CTA does.  Called by all threads of every CTA.
 __device__ __forceinline__ void start_status(const RowArgs& a) {
-  if (blockIdx.x != 0 || !a.status) return;
+  if (blockIdx.x != 0 || !a.status || a.keep_status) return;
   int bad = 0;
   if (a.single)
     for (int b = threadIdx.x; b < a.B; b += blockDim.x) bad |= a.lengths[b] < 0 || a.lengths[b] > a.T;
@@ -260,6 +260,12 @@ __host__ __device__ inline int teacher_table(int k) {
   int n = 64;
   while (n < 2 * k) n *= 2;
   return n;
+}
+
+// A label's first slot in the table: the high bits of a multiplicative hash, so
+// that labels with equal low bits spread too.
+__device__ __forceinline__ unsigned teacher_slot(int id, int size) {
+  return (unsigned)id * 2654435769u >> (__clz(size) + 1);
 }
 
 struct TeacherHead {
@@ -393,7 +399,7 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
     for (int j = lane; j < a.k; j += n) {
       const int id = tc.id[j];
       if (id < 0) continue;
-      for (unsigned at = (unsigned)id * 2654435769u;; ++at) {
+      for (unsigned at = teacher_slot(id, size);; ++at) {
         const int was = atomicCAS(&tc.table[at & (size - 1)], -1, id);
         if (was == id) twice = 1.0f;
         if (was == -1 || was == id) break;

@@ -534,6 +534,70 @@ def test_runs_are_identical_and_captured_graphs_replay(V, dtype):
             same(n, outs[n], want[n])
 
 
+WIDTHS = list(range(1, 140)) + [160, 200, 255, 256, 257, 260, 264, 300, 333, 511, 512, 513, 520, 700, 767,
+                                 1000, 1023, 1024, 1025, 1032, 1400, 2000, 2047, 2048, 2049, 2056, 2500,
+                                 4095, 4096, 4097, 5000, 8191, 8192, 8193, 9000]
+
+
+@pytest.mark.parametrize("dtype,pad", LAYOUTS + [(torch.float16, 8), (torch.float32, 4)],
+                         ids=lambda v: str(v).replace("torch.", ""))
+def test_every_width(dtype, pad):
+    """Each width takes its kernel, lanes and layout: log-probabilities with and
+    without a gradient, pairs and distillation with three list lengths, against
+    vectorised float64 forms."""
+    from semi_markov_crf_b200 import semicrf
+    B, T = 2, 3
+    lengths = torch.tensor([3, 2], dtype=torch.int32).cuda()
+    live = (torch.arange(T, device="cuda")[None] < lengths[:, None])[..., None]
+    for V in WIDTHS:
+        x, d = _logits(B, T, V, dtype, V, pad)
+        q = torch.softmax(d.double(), -1)
+        y = torch.randint(0, V, (B, T), generator=_gen(V), dtype=torch.int32).cuda()
+        hot = torch.zeros_like(q).scatter_(2, y.long()[..., None], 1.0)
+        base = torch.where(live, hot - q, torch.zeros_like(q)).cpu()
+        logp = torch.where(live[..., 0], q.gather(2, y.long()[..., None])[..., 0].log(),
+                           torch.zeros_like(q[..., 0])).cpu()
+        ones = torch.ones(B, T, dtype=torch.float64)
+        out = semicrf.label_logprob(d, lengths, y, grad=True)
+        bare = semicrf.label_logprob(d, lengths, y)
+        tol = lse_tol(V) + U * logp.abs()
+        _check(f"logp {V}", out["logp"], logp, tol)
+        _check(f"bare {V}", bare["logp"], logp, tol)
+        _check_grad(out["grad_logits"], base, ones, dtype, V, 1.0)
+        pairs = semicrf.preference_loss(d, lengths, y, beta=0.5)
+        w = 0.5 * ref.preference_term(float(pairs["reward"][0] - pairs["reward"][1]), 0.0)[1]
+        slope = torch.tensor([w, -w], dtype=torch.float64)[:, None] * ones
+        _check_grad(pairs["grad_logits"], slope[..., None] * base, slope.abs() * (1 + T), dtype, V, 1.0)
+        for k in (1, 20, 100):
+            if k > 2 * V + 4:
+                continue
+            ids = torch.randint(0, V, (B, T, k), generator=_gen(V + k), dtype=torch.int32).cuda()
+            t = torch.randn(B, T, k, generator=_gen(k)).cuda()
+            p = torch.softmax(t.double(), -1)
+            want = torch.where(live, q.scatter_add(2, ids.long(), -p), torch.zeros_like(q)).cpu()
+            dist = semicrf.distill_loss(d, lengths, ids, t)
+            _check_grad(dist["grad_logits"], want, ones, dtype, V, 1.0, 2.0)
+            loss = (p * (p.log() - q.gather(2, ids.long()).log())).sum(-1)
+            loss = torch.where(live[..., 0], loss, torch.zeros_like(loss)).cpu()
+            _check(f"token {V} {k}", dist["token_loss"], loss,
+                   (2 * lse_tol(V) + 60 * U) * (1 + loss.abs()) + U * loss.abs())
+
+
+@pytest.mark.parametrize("V,k", [(4096 * 40, 1024), (2048, 128), (2048, 700)])
+def test_teacher_labels_that_share_their_low_bits(V, k):
+    """Labels a power of two apart: the search for repeated ones stays short
+    (the time is not tested, the values are)."""
+    from semi_markov_crf_b200 import semicrf
+    B, T = 1, 2
+    x, d = _logits(B, T, V, torch.float32, V)
+    step = V // k
+    ids = (torch.arange(k) * step).int().expand(B, T, k).contiguous()
+    teacher = torch.randn(B, T, k, generator=_gen(1))
+    want = ref.distill_loss(x, [2], ids, teacher)
+    out = semicrf.distill_loss(d, torch.tensor([2], dtype=torch.int32).cuda(), ids.cuda(), teacher.cuda())
+    _check_distill(out, want, [2], torch.float32, V, 1.0)
+
+
 @pytest.mark.parametrize("V", [9, 300, 1300, 5000, 70000])
 def test_single_positions(V):
     """T = 1, the step that emits a label: the row pass writes the sequences'
