@@ -769,9 +769,13 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
     if (!hold || row <= (size_t)(s.slots - 1) * chunk || s.W == RING_WARPS) break;
   }
   s.cl = 1;
-  if (hold)
-    while (s.cl <= RING_CLUSTER_MAX && row > (size_t)s.cl * (s.slots - 1) * chunk) ++s.cl;
-  if (s.cl > RING_CLUSTER_MAX) return false;
+  if (hold && s.W == RING_WARPS) {
+    // a row takes at most 0.7 of the rings, so that the next one can follow it (90000
+    // bfloat16: 368 us on two CTAs, 401 on one whose ring it fills to 0.9) ...
+    const size_t ring = (s.slots - 1) * chunk;
+    while (s.cl < RING_CLUSTER_MAX && row * 10 > s.cl * ring * 7) ++s.cl;
+    if (row > s.cl * ring) return false;  // ... or all of the largest cluster's
+  }
   int resident;
   e = resident_clusters(kern, lim, dev, s.cl, resident);
   if (e != cudaSuccess) return true;
