@@ -9,8 +9,11 @@
 //   scalar    (one warp a group) joins the reducers' pairs (and, for a row wider
 //             than a ring, those of the CTAs of a cluster, through distributed
 //             shared memory), computes the position's terms, looks after the
-//             teacher's entries and the row's unaligned ends, and publishes what
-//             the writers need;
+//             row's unaligned ends, and publishes what the writers need;
+//   teachers  (distillation; two or three warps a group, which take its rows in
+//             turn) take the teacher's entries in ahead of the row, compute the
+//             position's loss and put the entries into the gradient behind the
+//             writers;
 //   writers   compute the gradient from the same chunks, still in shared
 //             memory, and give them back to the ring.
 // A row is read from memory once.  While its gradient is written the next row
@@ -36,7 +39,14 @@
 
 constexpr int RING_WARPS = 16;                      // reducers and writers of a CTA
 constexpr int RING_GROUPS = 8;                      // at most
-constexpr int RING_THREADS = (RING_WARPS + RING_GROUPS + 1) * 32;  // at most
+constexpr int RING_GROUPS_DISTILL = 4;              // at most, with its teacher warps:
+constexpr int TEACHERS_MAX = 3;
+__host__ __device__ constexpr int teacher_warps(int groups) { return groups == 4 ? 2 : TEACHERS_MAX; }
+template <int MODE>
+constexpr int ring_threads =  // at most
+    (RING_WARPS + 1 +
+     (MODE == LM_DISTILL ? RING_GROUPS_DISTILL * (1 + teacher_warps(RING_GROUPS_DISTILL))
+                         : RING_GROUPS)) * 32;
 constexpr int RING_NV = 4;                          // vectors of a chunk a thread takes
 constexpr int RING_WARP_BYTES = RING_NV * 32 * 16;  // a warp's part of a chunk
 constexpr int RING_SLOTS_MAX = 16;                  // chunks of a group's ring
@@ -54,15 +64,31 @@ struct RowNote {
   float at, scale, cy, gy;  // base, factor of the exponentials, addend and value at the label
   int y;                    // the label (-1: none)
   int kind;                 // NOTE_*
+  float sum;                // of the exponentials (for the teacher warps)
 };
 constexpr int NOTE_DIRECT = 0, NOTE_DIFFERENCE = 1, NOTE_ZERO = 2;
+
+// What a teacher warp tells the scalar warp about a row.
+struct TeacherNote {
+  float P;        // the entries' total probability
+  int malformed;  // an entry's label is outside the range
+};
+
+// float32 words of a teacher warp's entries.
+__host__ __device__ inline size_t teacher_entry(int k) {
+  return (size_t)TEACHER_WORDS * k + teacher_table(k);
+}
 
 struct GroupState {
   uint64_t full[RING_SLOTS_MAX], empty[RING_SLOTS_MAX];
   uint64_t red_full[2], red_free[2], note_full[2], note_free[2], peer[2];
+  // a teacher warp's own, a phase for each of its rows: barriers that alternate with
+  // all rows may be two phases on when it looks
+  uint64_t teacher_full[TEACHERS_MAX], told[TEACHERS_MAX], written[TEACHERS_MAX];
   float2 red[2][RING_WARPS];
   float2 part[2][RING_CLUSTER_MAX];
   RowNote note[2];
+  TeacherNote teacher[TEACHERS_MAX];
 };
 
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
@@ -216,6 +242,7 @@ struct RingPlace {
   GroupState* st;
   int first, units, rows;  // this group's rows: first, first + units, ...
   int rank, cl, slots, chunk_bytes;
+  int teachers;  // warps
 };
 
 // ---------------------------------------------------------------------- copier
@@ -344,6 +371,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
   Waiter wait{a.status, false};
   Cursor cur{0, 0};
   Turn turn{0, 0};
+  Cursor teacher{0, 0};
   const f32x2 sl2 = pair(a.sl, a.sl);
   for (int i = pl.first; i < pl.rows; i += pl.units) {
     const int r = pass_row<MODE>(i, pl.rows);
@@ -423,43 +451,35 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&st.note_free[turn.i]);
+    if (lane == 0) {
+      if (MODE == LM_DISTILL) mbar_arrive(&st.written[teacher.slot]);
+      mbar_arrive(&st.note_free[turn.i]);
+    }
+    if (MODE == LM_DISTILL) teacher.next(pl.teachers);
     turn.next();
   }
 }
 
 // ----------------------------------------------------------------- scalar warp
 template <typename T, int MODE, bool GRAD>
-__device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& pl, float* teachers,
-                                            int warps, int lane) {
-  constexpr int VE = vec_of<T>;
+__device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& pl, int warps, int lane) {
   constexpr bool PASS1 = MODE != LM_SCALED;
+  constexpr bool NOTES = GRAD || MODE == LM_DISTILL;
   GroupState& st = *pl.st;
   Waiter wait{a.status, false};
   Turn turn{0, 0}, rows_read{0, 0};
+  Cursor teacher{0, 0};
   HeadStream<MODE> heads{};
   heads.load(a, pl.first, pl.rows);
-  // the row whose teacher entries still have to be put into its gradient
-  bool due = false, due_repeats = false;
-  Base due_base{};
-  float due_scale = 0.0f, due_cq = 0.0f;
-  int due_row = 0;
-  Range due_range{};
-  const int tw = MODE == LM_DISTILL ? TEACHER_WORDS * a.k : 0;
-  auto teacher_at = [&](int i) {
-    float* t = teachers + i * tw;
-    return Teacher{t, reinterpret_cast<int*>(t + a.k), t + 2 * a.k, t + 3 * a.k,
-                   reinterpret_cast<int*>(teachers + 2 * tw)};
+  auto publish = [&](const RowNote& note) {
+    wait(&st.note_free[turn.i], turn.phase ^ 1);
+    __syncwarp();
+    if (lane == 0) {
+      st.note[turn.i] = note;
+      mbar_arrive(&st.note_full[turn.i]);
+      if (MODE == LM_DISTILL) mbar_arrive(&st.told[teacher.slot]);
+    }
   };
-  auto settle = [&](const Turn& then) {
-    // the writers are done with the row before this one
-    wait(&st.note_free[then.i], then.phase);
-    teacher_fix<T>(a, teacher_at(then.i), row_at<T>(a.g, due_row, a.ldg), due_base, due_scale, due_cq,
-                   due_repeats, lane, 32, due_range);
-    due = false;
-  };
-  TeacherAhead ahead{};
-  int ahead_row = -1;  // the row that `ahead` is of
   for (int i = pl.first; i < pl.rows; i += pl.units) {
     const int r = pass_row<MODE>(i, pl.rows);
     float w;
@@ -477,22 +497,12 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
     if (blank) {
       if (PASS1 && pl.rank == 0 && lane == 0) blank_outputs<MODE>(a, r, h.live);
       if (GRAD && !a.add && ei >= 0) g[ei] = from_f32<T>(0.0f);
+      // (this row's phase is taken note of)
+      if (MODE == LM_DISTILL) wait(&st.teacher_full[teacher.slot], teacher.phase);
     } else {
       const LabelIn<T> in = load_label<T, MODE>(a, r, h, x);
       T xe = from_f32<T>(0.0f);
       if (ei >= 0) xe = x[ei];
-      const Range rg = pl.rank == 0
-                           ? Range{0, p.sp.head + p.n * VE, p.sp.head + p.sp.nb * VE}
-                           : Range{p.sp.head + p.lo * VE, p.sp.head + (p.lo + p.n) * VE, a.V};
-      const Teacher tc = teacher_at(now.i);
-      TeacherHead th{};
-      if (MODE == LM_DISTILL) {
-        if (ahead_row != r) ahead.load(a, r, 0, lane, 32);
-        th = teacher_head<T>(a, r, in.lse, tc, ahead, x, g, rg, lane, 32, FULL_MASK);
-        ahead_row = r + pl.units;
-        if (ahead_row < pl.rows) ahead.load(a, ahead_row, 0, lane, 32);
-      }
-
       Base base;
       float S;
       if (PASS1) {
@@ -555,84 +565,112 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
         cy = (float)((double)w * a.s);
         cq = -cy;
       } else if (MODE == LM_DISTILL) {
-        P = th.P;
-        zero = th.malformed;
+        wait(&st.teacher_full[teacher.slot], teacher.phase);
+        P = st.teacher[teacher.slot].P;
+        zero = st.teacher[teacher.slot].malformed;
         cq = (float)(in.w * a.tau);
       } else {
         cy = label_outputs<MODE>(a, r, in, base, S, lane == 0 && pl.rank == 0);
         cq = -cy;
       }
       const float scale = __fdividef(cq * P, S);
-      if (GRAD) {
+      if (NOTES) {
         note.at = base.at;
         note.scale = scale;
         note.cy = cy;
+        note.sum = S;
         note.kind = zero ? NOTE_ZERO : base.direct ? NOTE_DIRECT : NOTE_DIFFERENCE;
         note.y = has_label(MODE) ? h.y : 0;  // >= 0: the row's chunks are in the ring
         if (has_label(MODE)) note.gy = based_exp(in.xy(), a.sl, base) * scale + cy;
-        // (published below, before the rest of this row's work)
-        wait(&st.note_free[now.i], now.phase ^ 1);
-        if (lane == 0) {
-          st.note[now.i] = note;
-          mbar_arrive(&st.note_full[now.i]);
-        }
-        if (ei >= 0) {
-          float gv = zero ? 0.0f : based_exp(to_f32<T>(xe), a.sl, base) * scale;
-          if (has_label(MODE) && ei == h.y) gv += cy;
-          if (a.add) gv += to_f32<T>(g[ei]);
-          g[ei] = from_f32<T>(gv);
-        }
+        publish(note);
       }
-      if (MODE == LM_DISTILL) {
-        if (zero) {
-          if (lane == 0 && pl.rank == 0) blank_outputs<MODE>(a, r, true);
-        } else {
-          teacher_terms(a, r, tc, th, base, S, pl.rank == 0, lane, 32, FULL_MASK);
-        }
-        __syncwarp();  // the edges are written
-        if (GRAD) {
-          Turn before = now;
-          before.i ^= 1;
-          before.phase ^= (uint32_t)before.i;
-          if (due) settle(before);
-          due = !zero;
-          due_base = base;
-          due_scale = scale;
-          due_cq = cq;
-          due_repeats = th.repeats;
-          due_row = r;
-          due_range = rg;
-        }
-        __syncwarp();
+      if (GRAD && ei >= 0) {
+        float gv = zero ? 0.0f : based_exp(to_f32<T>(xe), a.sl, base) * scale;
+        if (has_label(MODE) && ei == h.y) gv += cy;
+        if (a.add) gv += to_f32<T>(g[ei]);
+        g[ei] = from_f32<T>(gv);
       }
     }
-    if (GRAD) {
-      if (blank) {
-        if (MODE == LM_DISTILL && due) {
-          Turn before = now;
-          before.i ^= 1;
-          before.phase ^= (uint32_t)before.i;
-          settle(before);
-        }
-        wait(&st.note_free[now.i], now.phase ^ 1);
-        if (lane == 0) {
-          st.note[now.i] = note;
-          mbar_arrive(&st.note_full[now.i]);
-        }
+    if (NOTES) {
+      if (blank) publish(note);
+      if (MODE == LM_DISTILL) {
+        __syncwarp();  // the edges are written: the teacher warp may change them
+        if (GRAD && lane == 0) mbar_arrive(&st.written[teacher.slot]);
+        teacher.next(pl.teachers);
       }
       turn.next();
     }
   }
-  if (GRAD && MODE == LM_DISTILL && due) {
-    Turn before = turn;
-    before.i ^= 1;
-    before.phase ^= (uint32_t)before.i;
-    settle(before);
+}
+
+// --------------------------------------------------------------- teacher warps
+// Number `me` of pl.teachers, which take the group's rows in turn.  With the
+// entries in the scalar warp's hands the writers waited for the next row's
+// gathers: 2 x 1024 x 100003 float32 with 128 entries took 384 us, 333 with one
+// warp for the entries, 293 with three.
+template <typename T, bool GRAD>
+__device__ __forceinline__ void ring_teacher(const RowArgs& a, const RingPlace& pl, float* entries,
+                                             int me, int lane) {
+  constexpr int VE = vec_of<T>;
+  GroupState& st = *pl.st;
+  Waiter wait{a.status, false};
+  const int step = pl.units * pl.teachers;
+  const Teacher tc{entries, reinterpret_cast<int*>(entries + a.k), entries + 2 * a.k,
+                   entries + 3 * a.k, reinterpret_cast<int*>(entries + TEACHER_WORDS * a.k)};
+  HeadStream<LM_DISTILL> heads{};
+  TeacherAhead ahead{};
+  int n = me, ahead_row = -1;  // the row's number in the group; the row that `ahead` is of
+  uint32_t own = 1;            // parity of this warp's rows
+  heads.load(a, pl.first + me * pl.units, pl.rows);
+  for (int r = pl.first + me * pl.units; r < pl.rows; r += step, n += pl.teachers) {
+    float w;
+    bool blank;
+    const Head h = heads.take(a, w, blank);
+    heads.load(a, r + step, pl.rows);
+    const T* x = row_at<T>(a.x, r, a.ldx);
+    T* g = GRAD ? row_at<T>(a.g, r, a.ldg) : nullptr;
+    TeacherHead th{};
+    Range rg{};
+    float cq = 0.0f;
+    if (!blank) {
+      const LabelIn<T> in = load_label<T, LM_DISTILL>(a, r, h, x);
+      const Part p = part_of(x, a.V, pl.rank, pl.cl);
+      rg = pl.rank == 0 ? Range{0, p.sp.head + p.n * VE, p.sp.head + p.sp.nb * VE}
+                        : Range{p.sp.head + p.lo * VE, p.sp.head + (p.lo + p.n) * VE, a.V};
+      cq = (float)(in.w * a.tau);
+      if (ahead_row != r) ahead.load(a, r, 0, lane, 32);
+      th = teacher_head<T>(a, r, in.lse, tc, ahead, x, g, rg, lane, 32, FULL_MASK);
+      ahead_row = r + step;
+      if (ahead_row < pl.rows) ahead.load(a, ahead_row, 0, lane, 32);
+    }
+    __syncwarp();  // (accumulation: all have read the values that the writers will change)
+    if (lane == 0) {
+      st.teacher[me] = TeacherNote{th.P, th.malformed};
+      mbar_arrive(&st.teacher_full[me]);
+    }
+    own ^= 1;
+    const int i = n & 1;
+    wait(&st.told[me], own);
+    const RowNote note = st.note[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&st.note_free[i]);
+    if (blank) continue;
+    if (th.malformed) {
+      if (lane == 0 && pl.rank == 0) blank_outputs<LM_DISTILL>(a, r, true);
+      continue;
+    }
+    const Base base{note.at, note.kind == NOTE_DIRECT};
+    teacher_terms(a, r, tc, th, base, note.sum, pl.rank == 0, lane, 32, FULL_MASK);
+    if (GRAD) {
+      wait(&st.written[me], own);  // the row and its edges
+      teacher_fix<T>(a, tc, g, base, note.scale, cq, th.repeats, lane, 32, rg);
+    }
+    __syncwarp();
   }
 }
 
 template <typename T, int MODE, bool GRAD>
-__global__ void __launch_bounds__(RING_THREADS, 1)
+__global__ void __launch_bounds__(ring_threads<MODE>, 1)
     loss_ring_kernel(const __grid_constant__ RowArgs a, const RingShape shape) {
   extern __shared__ __align__(128) unsigned char ring_smem[];
   constexpr bool PASS1 = MODE != LM_SCALED;
@@ -649,7 +687,8 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
   pl.units = (int)(gridDim.x / pl.cl) * groups;
   const size_t ring_bytes = (size_t)pl.slots * pl.chunk_bytes;
   GroupState* states = reinterpret_cast<GroupState*>(ring_smem + groups * ring_bytes);
-  float* teachers = reinterpret_cast<float*>(states + groups);
+  float* entries = reinterpret_cast<float*>(states + groups);
+  pl.teachers = teacher_warps(groups);
   const int first = (int)(blockIdx.x / pl.cl) * groups;
 
   start_status(a);
@@ -663,8 +702,14 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
       mbar_init(&st.red_full[i], role_warps);
       mbar_init(&st.red_free[i], 1);
       mbar_init(&st.note_full[i], 1);
-      mbar_init(&st.note_free[i], role_warps);
+      // the writers and the row's teacher warp
+      mbar_init(&st.note_free[i], (GRAD ? role_warps : 0) + (MODE == LM_DISTILL ? 1 : !GRAD));
       mbar_init(&st.peer[i], 1);
+    }
+    for (int i = 0; i < TEACHERS_MAX; ++i) {
+      mbar_init(&st.teacher_full[i], 1);
+      mbar_init(&st.told[i], 1);
+      mbar_init(&st.written[i], role_warps + 1);  // the writers and, for the edges, the scalar warp
     }
     fence_mbar_init();
   }
@@ -677,13 +722,15 @@ __global__ void __launch_bounds__(RING_THREADS, 1)
     ring_copier<T, MODE>(a, ring_smem, states, groups, ring_bytes, pl, lane);
     return;
   }
-  const int gi = warp < RING_WARPS ? warp / W : warp - RING_WARPS;
+  const int teacher = warp - (RING_WARPS + groups + 1);
+  const int gi = warp < RING_WARPS ? warp / W : teacher < 0 ? warp - RING_WARPS : teacher / pl.teachers;
   pl.first = first + gi;
   pl.ring = ring_smem + gi * ring_bytes;
   pl.st = states + gi;
-  if (warp >= RING_WARPS) {
-    ring_scalar<T, MODE, GRAD>(a, pl, teachers + (size_t)gi * (MODE == LM_DISTILL ? 2 * TEACHER_WORDS * a.k + teacher_table(a.k) : 0),
-                               role_warps, lane);
+  if (MODE == LM_DISTILL && teacher >= 0) {
+    ring_teacher<T, GRAD>(a, pl, entries + teacher * teacher_entry(a.k), teacher % pl.teachers, lane);
+  } else if (warp >= RING_WARPS) {
+    ring_scalar<T, MODE, GRAD>(a, pl, role_warps, lane);
   } else {
     const int gw = warp - gi * W;
     if (BOTH) {
@@ -712,7 +759,7 @@ cudaError_t resident_clusters(K kern, RingLimits& lim, int dev, int cl, int& n) 
   if (dev < 8 && (n = lim.clusters[cl][dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(loss_sm_count() / cl * cl);
-  cfg.blockDim = dim3(RING_THREADS);
+  cfg.blockDim = dim3((RING_WARPS + 2 + TEACHERS_MAX) * 32);  // one group's, at most
   cfg.dynamicSmemBytes = RING_SMEM;
   cudaLaunchAttribute at = {};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -732,8 +779,9 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   const bool grad = a.g != nullptr && MODE != LM_PREFERENCE;
   const bool hold = grad && MODE != LM_SCALED;  // the row stays in the ring between the passes
   const size_t row = (size_t)a.V * sizeof(T);
-  const size_t entry =
-      MODE == LM_DISTILL ? (2ull * TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float) : 0;
+  auto entries = [&](int groups) {
+    return MODE == LM_DISTILL ? groups * teacher_warps(groups) * teacher_entry(a.k) * sizeof(float) : 0;
+  };
   const long long rows = (long long)a.B * a.T;
   static RingLimits limits[2];
   RingLimits& lim = limits[grad];
@@ -755,16 +803,16 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   // Warps a group: 8 KB of a row for each (rows in flight hide one another's
   // latency), all 16 where there are too few rows for more groups.
   RingShape s;
-  s.W = 2;
+  s.W = MODE == LM_DISTILL ? RING_WARPS / RING_GROUPS_DISTILL : 2;
   while (s.W < RING_WARPS &&
          (row > (size_t)s.W * 8 * 1024 || rows <= (long long)sms * (RING_WARPS / s.W) / 2 ||
-          RING_WARPS / s.W * entry > 64 * 1024))
+          entries(RING_WARPS / s.W) > 64 * 1024))
     s.W *= 2;
   size_t chunk, fixed;
   for (;; s.W *= 2) {
     const int groups = RING_WARPS / s.W;
     chunk = (size_t)(hold ? s.W / 2 : s.W) * RING_WARP_BYTES;
-    fixed = groups * (sizeof(GroupState) + entry);
+    fixed = groups * sizeof(GroupState) + entries(groups);
     s.slots = (int)std::min<size_t>(RING_SLOTS_MAX, (RING_SMEM - fixed) / groups / chunk);
     if (!hold || row <= (size_t)(s.slots - 1) * chunk || s.W == RING_WARPS) break;
   }
@@ -795,7 +843,7 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   }
   const int groups = RING_WARPS / s.W;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3((RING_WARPS + groups + 1) * 32);
+  cfg.blockDim = dim3((RING_WARPS + groups + 1 + (MODE == LM_DISTILL ? groups * teacher_warps(groups) : 0)) * 32);
   cfg.dynamicSmemBytes = groups * s.slots * chunk + fixed;
   cfg.stream = st;
   cudaLaunchAttribute at[2] = {};

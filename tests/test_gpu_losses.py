@@ -911,6 +911,56 @@ def test_streamed_rows_are_whole_and_the_same_every_time(op, rows, V, dtype):
             assert bool((err <= tol + 1e-30).all()), (b, t0, float((err - tol).max()))
 
 
+@pytest.mark.parametrize("B,T,V,dtype,k", [
+    (2000, 5, 16500, torch.bfloat16, 64), (500, 8, 40000, torch.bfloat16, 100),
+    (200, 9, 30000, torch.float32, 20), (200, 6, 70001, torch.float32, 130),
+    (120, 9, 100003, torch.float32, 40)])
+@pytest.mark.parametrize("grad", [True, False])
+def test_many_short_teacher_sequences(B, T, V, dtype, k, grad):
+    """Dozens of rows through each ring, rows that do not count (any number of
+    them in turn) and rows with a label outside the range among them."""
+    from semi_markov_crf_b200 import semicrf
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V + k)
+    tau = 1.5
+    d = torch.empty(B, T, V, dtype=dtype, device="cuda")
+    d.normal_(generator=g).mul_(2)
+    lens = torch.randint(0, T + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    lens[B // 3:B // 3 + 40] = 0
+    live = torch.arange(T, device="cuda") < lens[:, None]
+    ids = torch.randint(0, V // k, (B, T, k), generator=g, device="cuda", dtype=torch.int32) \
+        + torch.arange(k, device="cuda", dtype=torch.int32) * (V // k)
+    ids[..., 1] = torch.where(torch.rand(B, T, generator=g, device="cuda") < 0.3, ids[..., 0], ids[..., 1])
+    bad = torch.rand(B, T, generator=g, device="cuda") < 0.1
+    ids[..., k // 2] = torch.where(bad, V + 3, ids[..., k // 2])
+    teacher = torch.randn(B, T, k, generator=g, device="cuda")
+    w = torch.rand(B, generator=g, dtype=torch.float64, device="cuda") + 0.5
+    ws = semicrf.LossWorkspace(B, T)
+    out = semicrf.distill_loss(d, lens, ids, teacher, temperature=tau, grad_loss=w if grad else None,
+                               grad=grad, ws=ws)
+    assert semicrf.get_status(ws) == 0
+    token = out["token_loss"].double()
+    assert torch.equal(torch.isnan(token), bad & live)
+    assert bool((token[~live] == 0).all())
+    good = (live & ~bad).nonzero()
+    p = torch.softmax(teacher.double() / tau, -1)
+    for at in good.split(200):
+        b, t = at[:, 0], at[:, 1]
+        logq = torch.log_softmax(d[b, t].double() / tau, -1)
+        i = ids[b, t].long()
+        want = tau ** 2 * (p[b, t] * (p[b, t].log() - logq.gather(1, i))).sum(1)
+        tol = tau * tau * (2 * lse_tol(V) + 60 * U) * (1 + want.abs() / tau ** 2) + U * want.abs()
+        assert bool(((token[b, t] - want).abs() <= tol).all())
+        if grad:
+            a = tau * w[b][:, None]
+            want = a * logq.exp().scatter_add(1, i, -p[b, t])
+            tol = a * 2 * (3 * lse_tol(V) + 12 * U) + HALF[dtype] * want.abs()
+            assert bool(((out["grad_logits"][b, t].double() - want).abs() <= tol).all())
+    if grad:
+        for at in (~live | bad).nonzero().split(400):
+            assert not bool(out["grad_logits"][at[:, 0], at[:, 1]].any())
+
+
 def test_rows_beyond_32_bit_offsets():
     """More than 2^31 scores: the last rows against the same rows alone."""
     from semi_markov_crf_b200 import semicrf
