@@ -173,7 +173,7 @@ bool launch_cta(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   if (!grad && MODE != LM_DISTILL) return false;
   if (grad && ((px ^ pg) % 16 != 0 || (a.ldx - a.ldg) % vec_of<T> != 0)) return false;
   const size_t smem =
-      MODE == LM_DISTILL ? (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float) : 0;
+      MODE == LM_DISTILL ? (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k, a.V)) * sizeof(float) : 0;
   const unsigned rows = (unsigned)((long long)a.B * a.T);
   if (a.V <= 64 * CTA_NE) loss_cta_kernel<T, MODE, 64><<<rows, 64, smem, st>>>(a);
   else loss_cta_kernel<T, MODE, 128><<<rows, 128, smem, st>>>(a);

@@ -267,23 +267,14 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
       first[u] = now.ahead.id[u] >= 0;
     }
     bool repeats = true;
-    const int size = teacher_table(a.k);
+    const int size = teacher_table(a.k, V);
     if (size) {
-      // longer lists: a hash table tells whether a label comes twice at all (half
-      // empty, so that every probe ends)
-      for (int s = lane; s < size; s += L) tc.table[s] = -1;
+      teacher_clear(tc.table, size, V, lane, L);
       __syncwarp(mm);
       float twice = 0.0f;
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        const int id = now.ahead.id[u];
-        if (id < 0) continue;
-        for (unsigned at = teacher_slot(id, size);; ++at) {
-          const int was = atomicCAS(&tc.table[at & (size - 1)], -1, id);
-          if (was == id) twice = 1.0f;
-          if (was == -1 || was == id) break;
-        }
-      }
+      for (int u = 0; u < AHEAD; ++u)
+        if (now.ahead.id[u] >= 0 && teacher_again(tc.table, size, V, now.ahead.id[u])) twice = 1.0f;
       repeats = lanes_max(twice, L, mm) > 0.0f;
       if (!repeats)
 #pragma unroll
@@ -334,7 +325,7 @@ __global__ void __launch_bounds__(LANES_THREADS, lanes_ctas(NE))
   if (r >= rows) return;
   const unsigned mm = L == 32 ? FULL_MASK : ((1u << (L & 31)) - 1u) << ((tid & 31) / L * L);
   const int words = KEEP ? 0 : TEACHER_WORDS * a.k;
-  float* mine = dyn + (size_t)(tid / L) * (MODE == LM_DISTILL ? words + teacher_table(a.k) : 0);
+  float* mine = dyn + (size_t)(tid / L) * (MODE == LM_DISTILL ? words + teacher_table(a.k, a.V) : 0);
   const Teacher tc{mine, reinterpret_cast<int*>(mine + a.k), mine + 2 * a.k, mine + 3 * a.k,
                    reinterpret_cast<int*>(mine + words)};
   LaneLoad<T, NE, LAY, AHEAD> row;
@@ -349,7 +340,7 @@ cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
   size_t smem = 0;
   if (MODE == LM_DISTILL) {
     const size_t row =
-        (size_t)((KEEP ? 0 : TEACHER_WORDS * a.k) + teacher_table(a.k)) * sizeof(float);
+        (size_t)((KEEP ? 0 : TEACHER_WORDS * a.k) + teacher_table(a.k, a.V)) * sizeof(float);
     while (threads > 32 && threads / L * row > 48 * 1024) threads /= 2;
     smem = threads / L * row;
   }
@@ -428,7 +419,7 @@ bool launch_lanes(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
       return true;
     }
     // a lane holds its first entries in registers, and 48 KB hold a warp's rows
-    const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float);
+    const size_t row = (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k, a.V)) * sizeof(float);
     while (L < 32 && (a.k > TEACHER_AHEAD * L || 32 / L * row > 48 * 1024)) L *= 2;
   }
   e = with(std::integral_constant<int, 0>{}, L);

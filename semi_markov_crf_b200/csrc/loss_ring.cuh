@@ -75,8 +75,8 @@ struct TeacherNote {
 };
 
 // float32 words of a teacher warp's entries.
-__host__ __device__ inline size_t teacher_entry(int k) {
-  return (size_t)TEACHER_WORDS * k + teacher_table(k);
+__host__ __device__ inline size_t teacher_entry(int k, int V) {
+  return (size_t)TEACHER_WORDS * k + teacher_table(k, V);
 }
 
 struct GroupState {
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(ring_threads<MODE>, 1)
   pl.ring = ring_smem + gi * ring_bytes;
   pl.st = states + gi;
   if (MODE == LM_DISTILL && teacher >= 0) {
-    ring_teacher<T, GRAD>(a, pl, entries + teacher * teacher_entry(a.k), teacher % pl.teachers, lane);
+    ring_teacher<T, GRAD>(a, pl, entries + teacher * teacher_entry(a.k, a.V), teacher % pl.teachers, lane);
   } else if (warp >= RING_WARPS) {
     ring_scalar<T, MODE, GRAD>(a, pl, role_warps, lane);
   } else {
@@ -780,7 +780,7 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   const bool hold = grad && MODE != LM_SCALED;  // the row stays in the ring between the passes
   const size_t row = (size_t)a.V * sizeof(T);
   auto entries = [&](int groups) {
-    return MODE == LM_DISTILL ? groups * teacher_warps(groups) * teacher_entry(a.k) * sizeof(float) : 0;
+    return MODE == LM_DISTILL ? groups * teacher_warps(groups) * teacher_entry(a.k, a.V) * sizeof(float) : 0;
   };
   const long long rows = (long long)a.B * a.T;
   static RingLimits limits[2];

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
 
 template <typename T, int MODE>
 cudaError_t launch_wide(const RowArgs& a, cudaStream_t st) {
-  const size_t smem = MODE == LM_DISTILL ? (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k)) * sizeof(float) : 0;
+  const size_t smem = MODE == LM_DISTILL ? (size_t)(TEACHER_WORDS * a.k + teacher_table(a.k, a.V)) * sizeof(float) : 0;
   loss_wide_kernel<T, MODE><<<(unsigned)((long long)a.B * a.T), WIDE_THREADS, smem, st>>>(a);
   return cudaGetLastError();
 }
