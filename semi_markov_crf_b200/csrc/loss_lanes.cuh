@@ -371,7 +371,10 @@ cudaError_t launch_lanes_with(const RowArgs& a, int L, cudaStream_t st) {
   if constexpr (LAY == SPLIT) {
     if (L == 16) return launch_lanes_of<T, MODE, 16, LAY, KEEP>(a, st);
   }
-  if constexpr (KEEP == 4 && LAY != SPLIT) {  // lists that need four come with 8 lanes or more
+  if constexpr (KEEP == 4 && LAY == ELEMENTS) {
+    if (L == 4) return launch_lanes_of<T, MODE, 4, LAY, KEEP>(a, st);
+  }
+  if constexpr (KEEP == 4 && LAY != SPLIT) {  // lists that need four come with 4 or 8 lanes at least
     if (L == 8) return launch_lanes_of<T, MODE, 8, LAY, KEEP>(a, st);
     if (L == 16) return launch_lanes_of<T, MODE, 16, LAY, KEEP>(a, st);
   }
@@ -414,9 +417,11 @@ bool launch_lanes(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   };
   if constexpr (MODE == LM_DISTILL) {
     // Two or four entries a lane in registers rather than more lanes: 200000 rows of 38
-    // float32 with 17 entries take 52 us on 8 lanes, 78 on 16.
+    // float32 with 17 entries take 52 us on 8 lanes, 78 on 16; with 16 entries 39 us on
+    // 4 lanes, 46 on 8.  Four lanes with 32 elements each have no registers for it
+    // (100000 rows of 128 float32, 16 entries: 33 us, 31 on 8 lanes).
     if (a.k <= 128) {
-      while (L < 8 && a.k > 2 * L) L *= 2;
+      while (L < (vec ? 8 : 4) && a.k > 2 * L) L *= 2;
       while (a.k > 4 * L) L *= 2;
       e = a.k <= 2 * L ? with(std::integral_constant<int, 2>{}, L)
                        : with(std::integral_constant<int, 4>{}, L);
