@@ -701,6 +701,32 @@ def test_distill_list_lengths(V, dtype, k):
     _check_distill(out, want, [2, 2], dtype, V, 1.5)
 
 
+@pytest.mark.parametrize("dtype,pad", [(torch.float32, 0), (torch.float32, 1), (torch.bfloat16, 3)], ids=str)
+@pytest.mark.parametrize("V,k", [(17, 5), (38, 8), (38, 16), (38, 17), (38, 32), (64, 33), (64, 64),
+                                 (128, 16), (128, 40), (160, 65), (296, 128), (296, 129), (777, 20),
+                                 (2048, 5), (2049, 5), (2049, 17), (8200, 20), (8200, 200)])
+def test_one_repeated_teacher_label(V, k, dtype, pad):
+    """Positions without a repeated label and positions with one pair of them,
+    the lowest and the highest label, and neighbours across 32, among them."""
+    from semi_markov_crf_b200 import semicrf
+    B, T = 7, 9
+    lens = [T] * B
+    x, d = _logits(B, T, V, dtype, V + k, pad)
+    ids = torch.rand(B, T, V, generator=_gen(V * k)).argsort(-1)[..., :k].int()
+    pairs = [(0, 1), (0, k - 1), (k - 2, k - 1), (1, k // 2)]
+    for n in range(B * T):
+        row = ids[n // T, n % T]
+        if n % 3 == 0:
+            a, b = pairs[n % 4]
+            label = [0, V - 1, 31 % V, 32 % V, int(row[a])][n % 5]
+            row[row == label] = row[a].clone()      # its old place takes another
+            row[a] = row[b] = label
+    teacher = torch.randn(B, T, k, generator=_gen(k))
+    want = ref.distill_loss(x, lens, ids, teacher)
+    out = semicrf.distill_loss(d, torch.tensor(lens, dtype=torch.int32).cuda(), ids.cuda(), teacher.cuda())
+    _check_distill(out, want, lens, dtype, V, 1.0)
+
+
 @pytest.mark.parametrize("V,dtype", [(600001, torch.float32), (900001, torch.bfloat16)])
 def test_very_wide_rows(V, dtype):
     from semi_markov_crf_b200 import semicrf
