@@ -334,7 +334,9 @@ __device__ __forceinline__ void ring_reduce(const RowArgs& a, const RingPlace& p
       take_chunk<T>(raw, reinterpret_cast<const uint4*>(pl.ring + (size_t)cur.slot * pl.chunk_bytes),
                     gt, GT, n - c);
       const float nb = fmaxf(mb, Vec<T>::greatest(raw) * a.sl);
-      const float at = nb == NEG_INF ? 0.0f : nb;  // nothing above -inf yet: exponentials of 0
+      // nothing but masked scores yet: their exponentials around 0 are 0, as beside any
+      // score of a row whose base is direct (if there is none, the row is done again)
+      const float at = nb < -BASE_MAX ? 0.0f : nb;
       const f32x2 at2 = pair(-at, -at);
       f32x2 sum2[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
@@ -517,7 +519,7 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
         if (lane == 0) mbar_arrive(&st.red_free[rows_read.i]);
         if (ei >= 0) {
           const float xv = to_f32<T>(xe), eb = xv * a.sl;
-          join_pair(mb, s, eb, eb == NEG_INF ? 0.0f : ex2(fmaf(xv, a.sl, -eb)));
+          join_pair(mb, s, eb, eb < -BASE_MAX ? 0.0f : ex2(fmaf(xv, a.sl, -eb)));
         }
         join_lanes(mb, s);
         if (pl.cl > 1) {
@@ -542,17 +544,17 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
         }
         rows_read.next();
         base.at = mb;
-        base.direct = fabsf(mb) <= F32_MAX;
+        base.direct = fabsf(mb) <= BASE_MAX;
         S = s;
         if (!base.direct) {
-          // the scaled scores leave float32 (or the row holds nothing but -inf, or
-          // an infinity): once more over the row, differences first
+          // the scaled maximum is too far from 0 (or the row holds nothing but -inf,
+          // or an infinity): once more over the row, differences first
           float m = NEG_INF;
           for (int i = lane; i < a.V; i += 32) m = fmaxf(m, to_f32<T>(x[i]));
           m = warp_max(m);
-          S = 0.0f;
-          for (int i = lane; i < a.V; i += 32) S += ex2((to_f32<T>(x[i]) - m) * a.sl);
-          S = group_sum(S, 32);
+          double part = 0.0;  // a lane's terms are V / 32: too many for a float32 sum
+          for (int i = lane; i < a.V; i += 32) part += (double)ex2((to_f32<T>(x[i]) - m) * a.sl);
+          S = group_sum((float)part, 32);
           base.at = m;
         }
       } else {

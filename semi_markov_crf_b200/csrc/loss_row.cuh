@@ -56,19 +56,22 @@ __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000)
 // ------------------------------------------------------- exponentials of a row
 // Exponentials are taken in base 2 around the row's scaled maximum mb = m sl
 // (sl = log2(e) / temperature): 2^(x sl - mb), one fused multiply-add and one
-// ex2 an element.  Where m sl leaves float32's range (a row whose scores all
-// sit at the type's lowest value) they are 2^((x - m) sl) instead.
+// ex2 an element.  mb is rounded, and the product in the fused operation is
+// not: the greatest exponent is mb's rounding error, at most 1 up to BASE_MAX,
+// but beyond 2^31 enough to overflow (a row of nothing but a mask's -1e30).
+// There, and where m sl leaves float32, they are 2^((x - m) sl) instead.
 struct Base {
   float at;     // mb, or m where not direct
   bool direct;
 };
 
 constexpr float F32_MAX = 3.402823466e38f;
+constexpr float BASE_MAX = 16777216.0f;  // 2^24: half a step there is 1
 
 __device__ __forceinline__ Base make_base(float m, float sl) {
   const float mb = m * sl;
   Base h;
-  h.direct = fabsf(mb) <= F32_MAX;
+  h.direct = fabsf(mb) <= BASE_MAX;
   h.at = h.direct ? mb : m;
   return h;
 }

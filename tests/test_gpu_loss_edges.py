@@ -1,0 +1,268 @@
+"""GPU tests of the training losses over label scores where their inputs or
+sizes go wrong: masks of finite values, scores that are not numbers, positions
+without a teacher's entries, ratios far from 1, the limits of the temperature,
+calls without a gradient, very wide rows entry by entry.
+
+Tolerances (u = 2^-24), entry by entry, against float64 statements on the GPU.
+ * An exponential of the row: 2^-22 = 4 u for ex2, u |gap| each for the rounded
+   argument and for the rounded factor log2(e) / temperature, gap the entry's
+   distance from the row's maximum (natural logarithms).  Terms that matter in
+   a sum have gap <= 22: 48 u.
+ * The sum over a row: no term goes through more than V / 512 + 64 roundings
+   (a thread's running sum over its share of a row, then the joins).  So a
+   sum's relative error, the absolute one of its logarithm, is E(V) = (48 +
+   V / 512 + 64 + 4) u, the 4 u for the logarithm itself.
+ * A softmax entry q: E(V) + (4 + 2 gap) u, and 8 u for the factor, its
+   division and the product: (E(V) + (12 + 2 gap) u) q.  Below 2^-126 of the
+   maximum an exponential is 0.
+ * log-probabilities: E(V), and u |logp| for the output's rounding.
+ * Policy: with r the ratio and d = ref - logp, a term moves by |A| r (E + 12 u)
+   and c |e^d - 1| (E + 8 u) <= 2 c (E + 8 u) for the d here.
+ * Distillation: log p - log q is a difference of differences, 4 u of each
+   (|t - t_max| + |x - x_max|) / temperature and of itself; p carries
+   (2 |log p| + 28 + k / 32) u.
+ * One rounding to the output's type: half a step of it, and half a subnormal
+   step for float16.
+"""
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+TINY = {torch.float32: 0.0, torch.bfloat16: 0.0, torch.float16: 2.0 ** -25}
+# a width for each row kernel: lane groups, a CTA a row, rings, a cluster's
+# rings, and beyond them
+WIDTHS = [39, 1500, 5000, 40000, 140001, 600001]
+
+
+def sum_error(V):
+    return (48 + V / 512 + 64 + 4) * U
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _near(name, got, want, tol):
+    got, want = got.double(), want.double()
+    assert got.shape == want.shape, name
+    same = (got == want) | (torch.isnan(got) & torch.isnan(want))
+    off = ~same & ~((got - want).abs() <= tol)
+    assert not bool(off.any()), (
+        f"{name}: {int(off.sum())} of {off.numel()} off, first {got[off][0].item()} "
+        f"for {want[off][0].item()}, tolerance {torch.as_tensor(tol, device=got.device).expand_as(got)[off][0].item():.3e}")
+
+
+def _scores(B, T, V, dtype, seed, pad=0, scale=2.5):
+    x = torch.full((B, T, V + pad), math.nan, dtype=dtype, device="cuda")[..., :V]
+    x.copy_(scale * torch.randn(B, T, V, generator=_gen(seed), device="cuda"))
+    return x
+
+
+class Problem:
+    """Scores [B, T, V] with everything that the four losses take beside them,
+    their calls and their float64 statements."""
+
+    lo, hi, c, beta = 0.2, 0.3, 0.1, 0.3
+
+    def __init__(self, x, lens, tau=1.0, seed=0, k=20, lse=False, average=False, labels=None):
+        self.x, self.tau, self.lens, self.average = x, tau, list(lens), average
+        B, T, V = x.shape
+        self.B, self.T, self.V, self.k = B, T, V, min(k, V)
+        g = _gen(seed + 77)
+        self.lengths = torch.tensor(self.lens, dtype=torch.int32, device="cuda")
+        self.inside = torch.arange(T, device="cuda")[None] < self.lengths[:, None]
+        if labels is None:
+            labels = torch.randint(0, V, (B, T), generator=g, device="cuda", dtype=torch.int32)
+            if T > 2:
+                labels[:, 1] = -1
+        self.y = labels
+        self.counts = self.inside & (labels >= 0)
+        z = x.double()  # differences first: none is lost where a mask's value is all there is
+        z = (z - z.amax(-1, keepdim=True)) / tau
+        self.logq = torch.log_softmax(z, -1)
+        self.gap = -z
+        self.logp = torch.where(self.counts, self.logq.gather(-1, self.at())[..., 0],
+                                torch.zeros((), dtype=torch.float64, device="cuda"))
+        rnd = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.float64)
+        delta = 0.3 * rnd(B, T)
+        for corner in (math.log(1 - self.lo), math.log(1 + self.hi)):
+            delta = torch.where((delta - corner).abs() < 2e-3, delta + 5e-3, delta)
+        self.old = (self.logp - delta).float()
+        self.ref = (self.logp + 0.2 * rnd(B, T)).float()
+        self.adv = rnd(B, T).clamp(-2, 2).float()
+        self.w = torch.rand(B, generator=g, device="cuda", dtype=torch.float64) + 0.5
+        t = 0.8 * x.float() + tau * torch.randn(B, T, V, generator=g, device="cuda")
+        top = torch.nan_to_num(t).topk(self.k, -1)
+        self.ids, self.teacher = top.indices.int(), top.values.contiguous()
+        self.ids[..., -1] = self.ids[..., 0]  # one label comes twice
+        self.lse = None
+        if lse:
+            self.lse = ((self.teacher.double() / tau).logsumexp(-1) + 0.3).float()
+
+    def at(self):
+        return self.y.clamp_min(0).long()[..., None]
+
+    def call(self, op, grad=True, accumulate=False, pad=0, fill=math.nan, **kw):
+        from semi_markov_crf_b200 import semicrf
+        if grad:
+            buf = torch.full((self.B, self.T, self.V + pad), fill, dtype=self.x.dtype, device="cuda")
+            buf = buf[..., :self.V]
+            if accumulate:
+                buf.copy_(torch.randn(buf.shape, generator=_gen(5), device="cuda"))
+                self.start = buf.double()
+            kw["out"] = {"grad_logits": buf}
+        kw.update(temperature=self.tau, grad=grad, accumulate=accumulate)
+        if op == "logprob":
+            return semicrf.label_logprob(self.x, self.lengths, self.y,
+                                         grad_logp=self.adv if grad else None, **kw)
+        if op == "policy":
+            return semicrf.policy_loss(self.x, self.lengths, self.y, self.old, self.adv,
+                                       ref_logp=self.ref, clip_low=self.lo, clip_high=self.hi,
+                                       kl_coef=self.c, grad_loss=self.w, **kw)
+        if op == "preference":
+            return semicrf.preference_loss(self.x, self.lengths, self.y, self.ref, beta=self.beta,
+                                           margin=0.1, smoothing=0.1, average=self.average,
+                                           grad_loss=self.w[:self.B // 2].contiguous(), **kw)
+        return semicrf.distill_loss(self.x, self.lengths, self.ids, self.teacher,
+                                    teacher_lse=self.lse, grad_loss=self.w, **kw)
+
+    def check(self, op, out, accumulated=False, where=None):
+        """Every output against its statement; `where` [B, T]: only these rows'
+        gradients."""
+        V, B, tau, E = self.V, self.B, self.tau, sum_error(self.V)
+        zero = torch.zeros((), dtype=torch.float64, device="cuda")
+        live = lambda v: torch.where(self.counts, v, zero)
+        if op != "distill":
+            _near("logp", out["logp"], self.logp, E + U * self.logp.abs())
+        points = self.at()
+        if op == "logprob":
+            e = live(E + U * self.logp.abs())
+            s = self.logp.sum(1)
+            _near("score", out["score"], s, e.sum(1) + U * s.abs())
+            a = live(self.adv.double())
+            err, p = a.abs() * 2 * U, torch.ones_like(points, dtype=torch.float64)
+        elif op == "policy":
+            A, old, ref = self.adv.double(), self.old.double(), self.ref.double()
+            r, d = (self.logp - old).exp(), ref - self.logp
+            kl = live(torch.expm1(d) - d)
+            free, cut = r * A, r.clamp(1 - self.lo, 1 + self.hi) * A
+            term = live(-torch.minimum(free, cut)) + self.c * kl
+            held = (cut < free) & self.counts
+            ekl = live(2 * (E + 8 * U) + U * kl)
+            e = live(A.abs() * r * (E + 12 * U)) + self.c * ekl + U * term.abs()
+            _near("loss", out["loss"], term.sum(1), e.sum(1) + U * term.sum(1).abs())
+            _near("kl", out["kl"], kl.sum(1), ekl.sum(1) + U * kl.sum(1))
+            assert torch.equal(out["clipped"], held.sum(1).int())
+            w = self.w[:, None]
+            a = w * live(torch.where(held, zero, -free) - self.c * torch.expm1(d))
+            err = w * (live(A.abs() * r * (E + 12 * U)) + self.c * live(2 * (E + 8 * U) + zero)) \
+                + 2 * U * a.abs()
+            p = torch.ones_like(points, dtype=torch.float64)
+        elif op == "preference":
+            ratio = live(self.logp - self.ref.double())
+            n = self.counts.sum(1).clamp_min(1).double() if self.average else torch.ones(B).cuda()
+            reward = self.beta * ratio.sum(1) / n
+            e = self.beta * (live(E + U * ratio.abs())).sum(1) / n + U * reward.abs()
+            _near("reward", out["reward"], reward, e + U * reward.abs())
+            P = B // 2
+            u = reward[:P] - reward[P:] - 0.1
+            sig = torch.nn.functional.logsigmoid
+            loss = -0.9 * sig(u) - 0.1 * sig(-u)
+            eu = e[:P] + e[P:]
+            _near("loss", out["loss"], loss, eu + U * loss.abs())
+            slope = (-0.9 * torch.sigmoid(-u) + 0.1 * torch.sigmoid(u)) * self.beta * self.w[:P]
+            a = live(torch.cat([slope, -slope])[:, None] / n[:, None])
+            err = live((torch.cat([eu, eu]) * 0.25 * self.beta * torch.cat([self.w[:P]] * 2)
+                        / n)[:, None] + zero) + 2 * U * a.abs()
+            p = torch.ones_like(points, dtype=torch.float64)
+        else:
+            t = self.teacher.double() / tau
+            if self.lse is None:
+                logt = torch.log_softmax(t - t.amax(-1, keepdim=True), -1)
+            else:
+                logt = t - self.lse.double()[..., None]
+            p, i = logt.exp(), self.ids.long()
+            points = i
+            gap = logt - self.logq.gather(-1, i)
+            inside = lambda v: torch.where(self.inside, v, zero)
+            token = inside(tau ** 2 * (p * gap).sum(-1))
+            dt = t.amax(-1, keepdim=True) - t
+            ep = (2 * dt + 28 + self.k / 32) * U
+            e = p * (E + 4 * U * (dt + self.gap.gather(-1, i) + gap.abs())) + p * gap.abs() * ep
+            e = inside(tau ** 2 * (e.sum(-1) + 40 * U)) + U * token.abs()
+            _near("token_loss", out["token_loss"], token, e)
+            _near("loss", out["loss"], token.sum(1), e.sum(1) + U * token.sum(1).abs())
+            a = inside(-tau * tau * self.w[:, None] + 0 * token)  # over temperature, below
+            err, p = a.abs() * 60 * U, p
+        if "grad_logits" not in out:
+            return
+        dtype = self.x.dtype
+        rows = (a != 0 if where is None else where & (a != 0)).nonzero()
+        got = out["grad_logits"]
+        for b, t in rows.tolist():
+            q = self.logq[b, t].exp()
+            f = a[b, t] / tau
+            total = p[b, t].sum() if op == "distill" else 1.0
+            # equal labels add up
+            hot = torch.zeros_like(q).scatter_add_(0, points[b, t], p[b, t])
+            want = f * (hot - total * q)
+            tol = (f.abs() * total * q * (E + (12 + 2 * self.gap[b, t]) * U)
+                   + f.abs() * hot * (80 + self.k / 32) * U
+                   + err[b, t] / tau * (q * total + hot) + f.abs() * 2.0 ** -120)
+            if op == "distill":
+                dt = (self.teacher[b, t].amax() - self.teacher[b, t]).double() / tau
+                tol += f.abs() * torch.zeros_like(q).scatter_add_(0, points[b, t],
+                                                                  p[b, t] * 2 * dt * U)
+            if accumulated:
+                want = want + self.start[b, t]
+                tol += 3 * U * (self.start[b, t].abs() + want.abs())
+            _near(f"gradient of row {b}, {t}", got[b, t], want,
+                  tol + HALF[dtype] * want.abs() + TINY[dtype])
+        rest = (a == 0 if where is None else where & (a == 0)).nonzero()
+        for b, t in rest.tolist():
+            want = self.start[b, t] if accumulated else torch.zeros(V, dtype=torch.float64).cuda()
+            _near(f"gradient of row {b}, {t}", got[b, t], want, 0.0)
+
+
+OPS = ["logprob", "policy", "preference", "distill"]
+
+
+MASKS = {torch.float32: [-1e9, -1e10, -1e30, torch.finfo(torch.float32).min],
+         torch.bfloat16: [-1e10, -1e30, torch.finfo(torch.bfloat16).min],
+         torch.float16: [-65504.0]}
+
+
+@pytest.mark.parametrize("dtype", list(MASKS), ids=str)
+@pytest.mark.parametrize("tau", [1.0, 2.0, 0.5, 1e-3, 1e3])
+@pytest.mark.parametrize("V", WIDTHS)
+def test_masks_of_finite_values(V, tau, dtype):
+    """Masks of any finite value: labels of probability zero beside ordinary
+    scores, wherever in the row they are; a row of nothing but the mask's value,
+    however large, is uniform."""
+    B, T = 2, 4
+    labels = torch.tensor([[V - 1, 0, V // 2, V - 2], [V // 3, 1, V // 2, 0]], dtype=torch.int32).cuda()
+    for value in MASKS[dtype]:
+        x = _scores(B, T, V, dtype, V)
+        x[0, 0, :V // 2] = value           # the first half
+        x[0, 1, V // 2:] = value           # the last half
+        x[0, 2, :V // 2] = value           # all but one
+        x[0, 2, V // 2 + 1:] = value
+        x[0, 3] = value                    # all of them
+        x[1, 0] = -value                   # a uniform row far up
+        x[1, 1, ::2] = value               # every second
+        x[1, 2] += value / 4               # a common offset
+        p = Problem(x, [T, T], tau=tau, seed=V, labels=labels, k=9)
+        p.w *= 0.5
+        for op in OPS:
+            p.check(op, p.call(op))
+        for op in OPS:
+            p.check(op, p.call(op, grad=False))
