@@ -436,8 +436,9 @@ SEMICRF_API int semicrf_preference_loss(const void *logits, int dtype, int64_t l
  *   token_loss[b, t] = temperature^2 sum_j p_j (log p_j - log q_{id_j})
  *   loss[b] = sum_t token_loss[b, t],  grad_logits = grad_loss[b] d loss[b] / d logits.
  * Entries of equal label add up; an entry of logit -inf has p = 0; a position
- * with no entry of positive probability has loss and gradient 0.  An id >= V
- * gives NaN and no gradient row.  loss and token_loss are nullable.
+ * with no entry of positive probability has loss and gradient 0, whatever its
+ * scores and teacher_lse are.  An id >= V gives NaN and no gradient row.  loss
+ * and token_loss are nullable.
  */
 SEMICRF_API int semicrf_distill_loss(const void *logits, int dtype, int64_t ld,
                                      const int32_t *lengths, const int32_t *teacher_ids,

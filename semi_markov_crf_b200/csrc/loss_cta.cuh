@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(L, 640 / L)
     th = teacher_head<T>(a, r, in.lse, tc, ahead, x, g, all, lane, 32, FULL_MASK);
     if (lane == 0) {
       tshare[0] = th.P;
-      tshare[1] = th.malformed ? 1.0f : 0.0f;
+      tshare[1] = th.malformed ? 1.0f : th.none ? 2.0f : 0.0f;
     }
   }
 
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(L, 640 / L)
   if (MODE == LM_SCALED) base = unpack_stat(in.stat, S);
   else base = make_base(cta_max<L>(fmaxf(Vec<T>::greatest(q), xe), red[0]), a.sl);
   if (MODE == LM_DISTILL && tshare[1] != 0.0f) {
-    if (tid == 0) blank_outputs<MODE>(a, r, true);
+    if (tid == 0) blank_outputs<MODE>(a, r, tshare[1] == 1.0f);
     fill_zero();
     return;
   }

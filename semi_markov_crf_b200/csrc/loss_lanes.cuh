@@ -124,7 +124,8 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
     } else {
       th = teacher_head<T>(a, r, now.in.lse, tc, now.ahead, x, g, all, lane, L, mm);
     }
-    blank = malformed = th.malformed;
+    malformed = th.malformed;
+    blank = malformed || th.none;
   }
   if (blank) {
     if (MODE != LM_SCALED && lane == 0) blank_outputs<MODE>(a, r, malformed);

@@ -298,6 +298,7 @@ struct TeacherHead {
   float tm, pT, P;
   double tlog;
   bool malformed;
+  bool none;     // no entry has a probability: no loss and no gradient
   bool repeats;  // two entries may have the same label
 };
 
@@ -336,9 +337,13 @@ using TeacherAhead = TeacherLoad<TEACHER_AHEAD>;
 
 // Total probability of a teacher whose greatest logit is tm and whose
 // exponentials around it sum to s: an entry's probability is its exponential
-// times pT.
+// times pT.  Without an entry in use s is 0, and the log-sum-exp is not looked at.
 __device__ __forceinline__ void teacher_total(const RowArgs& a, float lse, float s, TeacherHead& th) {
-  if (a.tlse) {
+  th.none = s == 0.0f;
+  if (th.none) {
+    th.tlog = 0.0;
+    th.pT = th.P = 0.0f;
+  } else if (a.tlse) {
     th.tlog = (double)lse - (double)th.tm * a.s;
     const float hi = (float)th.tlog;
     th.pT = expf(-hi) * (1.0f - (float)(th.tlog - (double)hi));
@@ -346,7 +351,7 @@ __device__ __forceinline__ void teacher_total(const RowArgs& a, float lse, float
   } else {
     th.tlog = log_of_sum(s);
     th.pT = 1.0f / s;
-    th.P = s > 0.0f ? 1.0f : s;  // no entry with a probability: no loss, no gradient
+    th.P = s > 0.0f ? 1.0f : s;  // NaN stays
   }
 }
 

@@ -51,11 +51,12 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
       th = teacher_head<T>(a, r, a.tlse ? a.tlse[r] : 0.0f, tc, ahead, x, g, all, lane, 32, FULL_MASK);
       if (lane == 0) {
         tshare[0] = th.P;
-        tshare[1] = th.malformed ? 1.0f : 0.0f;
+        tshare[1] = th.malformed ? 1.0f : th.none ? 2.0f : 0.0f;
       }
     }
     __syncthreads();
     blank = tshare[1] != 0.0f;
+    malformed = tshare[1] == 1.0f;
   }
   if (blank) {
     if (MODE != LM_SCALED && tid == 0) blank_outputs<MODE>(a, r, malformed);

@@ -266,3 +266,39 @@ def test_masks_of_finite_values(V, tau, dtype):
             p.check(op, p.call(op))
         for op in OPS:
             p.check(op, p.call(op, grad=False))
+
+
+@pytest.mark.parametrize("lse", [-math.inf, -100.0, math.nan, 3.0, None], ids=str)
+@pytest.mark.parametrize("V", WIDTHS)
+def test_positions_without_teacher_entries(V, lse):
+    """No loss and no gradient where a position has no entry of positive
+    probability, whatever the teacher's log-sum-exp and the scores are there; the
+    other positions have theirs."""
+    x = _scores(2, 4, V, torch.float32, V)
+    x[1, 1, V // 2] = math.nan
+    x[1, 2] = -math.inf
+    empty = torch.tensor([[1, 1, 0, 1], [0, 1, 1, 0]], dtype=torch.bool, device="cuda")
+    p = Problem(torch.nan_to_num(x), [4, 3], tau=1.5, seed=V, lse=lse is not None)
+    p.x = x
+    p.ids[0, 0] = -1
+    p.teacher[0, 1] = -math.inf
+    p.ids[0, 3, ::2] = -5
+    p.teacher[0, 3, 1::2] = -math.inf
+    p.teacher[0, 3, ::2] = math.nan     # behind an unused entry
+    p.ids[1, 1:3] = -1
+    if lse is not None:
+        p.lse[empty] = lse
+    for accumulate in (False, True):
+        out = p.call("distill", accumulate=accumulate)
+        assert bool((out["token_loss"][empty] == 0).all())
+        start = p.start if accumulate else torch.zeros_like(out["grad_logits"]).double()
+        assert torch.equal(out["grad_logits"][empty].double(), start[empty])
+        assert torch.isfinite(out["loss"]).all()
+        q = Problem(torch.nan_to_num(x), [4, 3], tau=1.5, seed=V, lse=lse is not None)
+        want = q.call("distill", accumulate=accumulate)
+        full = ~empty
+        assert torch.equal(out["token_loss"][full], want["token_loss"][full])
+        assert torch.equal(out["grad_logits"][full], want["grad_logits"][full])
+    out = p.call("distill", grad=False)
+    assert bool((out["token_loss"][empty] == 0).all())
+    assert torch.isfinite(out["loss"]).all()
