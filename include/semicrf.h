@@ -414,7 +414,9 @@ SEMICRF_API int semicrf_policy_loss(const void *logits, int dtype, int64_t ld,
  *   loss[i] = -(1 - smoothing) log sigmoid(u_i) - smoothing log sigmoid(-u_i)
  * grad_logits = grad_loss[i] * d loss[i] / d logits; grad_loss, loss [B/2].
  * loss, reward and logp [B, T] (float32) are nullable.  A malformed sequence
- * (a label >= V, a bad length) gives its pair loss NaN and no gradient.
+ * (a label >= V, a bad length) gives its pair loss NaN and no gradient.  A pair
+ * whose loss is NaN for its numbers (a row without a softmax, a NaN ref_logp) has
+ * a NaN gradient in all rows of both sequences that count.
  */
 SEMICRF_API int semicrf_preference_loss(const void *logits, int dtype, int64_t ld,
                                         const int32_t *lengths, const int32_t *labels, int B,

@@ -74,7 +74,8 @@ size_t loss_layout(int B, int T, void* base, LossWs* p);
 struct SeqArgs {
   int B, T;
   const int32_t* lengths;
-  const int32_t* labels;   // LM_PREFERENCE: which positions count (for the mean)
+  const int32_t* labels;   // LM_PREFERENCE: which positions count, which are malformed
+  int V;
   int* status;
   const float* tok;
   const float* kl;

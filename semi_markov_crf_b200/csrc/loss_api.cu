@@ -247,6 +247,7 @@ extern "C" int semicrf_preference_loss(const void* logits, int dtype, int64_t ld
   q.T = T;
   q.lengths = lengths;
   q.labels = labels;
+  q.V = V;
   q.status = p.status;
   q.tok = p.tok;
   q.beta = beta;

@@ -302,3 +302,67 @@ def test_positions_without_teacher_entries(V, lse):
     out = p.call("distill", grad=False)
     assert bool((out["token_loss"][empty] == 0).all())
     assert torch.isfinite(out["loss"]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("V", WIDTHS)
+def test_scores_that_are_not_numbers(V, dtype):
+    """A row that holds NaN or +inf, or nothing but -inf, makes its loss and its
+    gradient row NaN, so that a step that looks for them sees them: for a pair
+    the rows of both its sequences that count.  Other sequences and pairs keep
+    theirs."""
+    B, T = 6, 3
+    clean = _scores(B, T, V, dtype, V)
+    for value in ("nan", "inf", "none"):
+        p = Problem(clean, [3, 2, 3, 3, 2, 3], seed=V)
+        x = clean.clone()
+        if value == "none":
+            x[1, 0] = -math.inf
+        else:
+            x[1, 0, V // 3] = float(value)
+        p.x = x
+        for op in ("logprob", "policy", "distill"):
+            out = p.call(op)
+            g = out["grad_logits"]
+            assert bool(torch.isnan(g[1, 0]).all()), (value, op)
+            loss = out["score" if op == "logprob" else "loss"]
+            assert torch.isnan(loss).tolist() == [False, True] + [False] * 4, (value, op)
+            keep = torch.ones(B, T, dtype=torch.bool, device="cuda")
+            keep[1, 0] = False
+            assert torch.isfinite(g[keep]).all(), (value, op)
+            bare = p.call(op, grad=False)
+            assert torch.isnan(bare["score" if op == "logprob" else "loss"]).tolist() \
+                == torch.isnan(loss).tolist(), (value, op)
+        out = p.call("preference")
+        assert torch.isnan(out["loss"]).tolist() == [False, True, False], value
+        assert torch.isnan(out["reward"]).tolist() == [False, True] + [False] * 4, value
+        g = out["grad_logits"]
+        for b in (1, 4):
+            for t in range(T):
+                if bool(p.counts[b, t]):
+                    assert bool(torch.isnan(g[b, t]).all()), (value, b, t)
+                else:
+                    assert not bool(g[b, t].any()), (value, b, t)
+        for b in (0, 2, 3, 5):
+            assert torch.isfinite(g[b]).all(), (value, b)
+        # a malformed label takes the pair's gradient away all the same
+        p.y = p.y.clone()
+        p.y[4, 0] = V
+        out = p.call("preference")
+        assert torch.isnan(out["loss"]).tolist() == [False, True, False], value
+        assert not bool(out["grad_logits"][[1, 4]].any()), value
+        assert bool(out["grad_logits"][[0, 2]].any())
+
+
+def test_a_reference_that_is_not_a_number():
+    """A NaN in ref_logp reaches its pair's loss and gradient."""
+    p = Problem(_scores(4, 3, 50, torch.float32, 1), [3, 3, 3, 3])
+    p.ref[0, 0] = math.nan
+    out = p.call("preference")
+    assert torch.isnan(out["loss"]).tolist() == [True, False]
+    g = out["grad_logits"]
+    assert bool(torch.isnan(g[[0, 2]][:, [0, 2]]).all()) and torch.isfinite(g[[1, 3]]).all()
+    p.ref[0, 1] = math.nan     # a position that does not count is not read
+    p.ref[0, 0] = -1.0
+    out = p.call("preference")
+    assert torch.isfinite(out["loss"]).all() and torch.isfinite(out["grad_logits"]).all()
