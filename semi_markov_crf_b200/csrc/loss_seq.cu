@@ -135,30 +135,39 @@ __global__ void __launch_bounds__(SUM_THREADS) loss_pairs_kernel(SeqArgs a, int 
   if (ctas > 1) cluster_sync();  // the peers are running
   after_previous();
   double reward[2], inv[2];
-  bool off[2], wrong[2];
+  bool off[2];
   for (int side = 0; side < 2; ++side) {
     const int b = i + side * P;
     const int L = a.lengths[b];
     off[side] = L < 0 || L > a.T;
     const long long row = (long long)b * a.T;
-    double out[3];
-    sequence_sums<3>(off[side] ? 0 : L, rank, ctas, st, [&](int k, int t) -> double {
+    double out[2];
+    sequence_sums<2>(off[side] ? 0 : L, rank, ctas, st, [&](int k, int t) -> double {
       if (k == 0) return (double)a.tok[row + t];
-      if (k == 1) return a.average && a.labels[row + t] >= 0 ? 1.0 : 0.0;
-      return a.labels[row + t] >= a.V ? 1.0 : 0.0;
+      return a.average && a.labels[row + t] >= 0 ? 1.0 : 0.0;
     }, out);
     if (ctas > 1) cluster_sync();  // CTA 0 has read the other side's sums
-    wrong[side] = off[side] || out[2] > 0.0;
     inv[side] = 1.0 / fmax(out[1], 1.0);
     reward[side] = a.beta * out[0] * inv[side];
   }
-  if (rank != 0 || threadIdx.x != 0) return;
+  if (rank != 0) return;
+  const double u = reward[0] - reward[1] - a.margin;
+  // A pair with a malformed sequence has loss NaN and no gradient; one whose loss is
+  // NaN for its numbers has a NaN gradient, for whoever looks for that.  A malformed
+  // label shows in the sum, so that few pairs have theirs searched.
+  bool none = off[0] || off[1];
+  if (!none && u != u) {
+    int wrong = 0;
+    for (int side = 0; side < 2; ++side) {
+      const int b = i + side * P, L = a.lengths[b];
+      for (int t = threadIdx.x; t < L; t += blockDim.x) wrong |= a.labels[(long long)b * a.T + t] >= a.V;
+    }
+    none = __syncthreads_or(wrong);
+  }
+  if (threadIdx.x != 0) return;
   double loss, slope;
-  logistic(reward[0] - reward[1] - a.margin, a.smoothing, loss, slope);
+  logistic(u, a.smoothing, loss, slope);
   const double w = (a.w ? a.w[i] : 1.0) * a.beta * slope;
-  // a pair with a malformed sequence has loss NaN and no gradient; one whose loss is
-  // NaN for its numbers has a NaN gradient, for whoever looks for that
-  const bool none = wrong[0] || wrong[1];
   if (off[0] || off[1]) set_status(a.status, ST_BAD_LENGTH);
   if (a.loss) a.loss[i] = none ? quiet_nan() : (float)loss;
   for (int side = 0; side < 2; ++side) {
