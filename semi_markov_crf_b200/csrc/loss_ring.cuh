@@ -406,7 +406,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
         const uint4* chunk =
             reinterpret_cast<const uint4*>(pl.ring + (size_t)cur.slot * pl.chunk_bytes);
         const int have = p.n - c;
-        if (note.kind == NOTE_ZERO) {  // read, but its teacher's entries leave nothing
+        if (MODE == LM_DISTILL && note.kind == NOTE_ZERO) {  // read, but its teacher's entries leave nothing
           give_back(&st.empty[cur.slot], lane);
           clear(c, min(have, chunk_vecs));
         } else if (plain) {
