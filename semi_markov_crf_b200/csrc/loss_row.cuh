@@ -223,24 +223,24 @@ template <int MODE, typename T>
 __device__ __forceinline__ float label_outputs(const RowArgs& a, long long r, const LabelIn<T>& in,
                                                const Base& h, float S, bool writer) {
   const double logp = ((double)in.xy() - base_score(h, a.inv_sl)) * a.s - log_of_sum(S);
-  float slope = in.slope;
+  double slope = (double)in.slope;
   float term = (float)logp;
   if (MODE == LM_PREFERENCE) term = (float)(logp - (double)in.ref_logp);
   if (MODE == LM_POLICY) {
-    const PolicyTerm<float> o =
-        policy_term<float>((float)(logp - (double)in.old_logp), in.adv, (float)a.clip_lo,
-                           (float)a.clip_hi, (float)a.kl_coef, a.ref_logp != nullptr,
-                           (float)((double)in.ref_logp - logp));
-    term = o.loss;
+    const bool has_ref = a.ref_logp != nullptr;
+    const PolicyTerm<double> o =
+        policy_term_of(logp - (double)in.old_logp, (double)in.adv, a.clip_lo, a.clip_hi, a.kl_coef,
+                       has_ref, has_ref ? (double)in.ref_logp - logp : 0.0);
+    term = (float)o.loss;
     slope = o.slope;
-    if (writer) put_policy(a, r, o.kl, o.clipped);
+    if (writer) put_policy(a, r, (float)o.kl, o.clipped);
   }
   if (writer) {
     put_term(a, r, term);
     if (a.logp) a.logp[r] = (float)logp;
     if (MODE == LM_PREFERENCE) a.stat[r] = pack_stat(h, S);
   }
-  return (float)(in.w * (double)slope * a.s);
+  return (float)(in.w * slope * a.s);
 }
 
 // ------------------------------------------------------ the teacher's entries

@@ -366,3 +366,63 @@ def test_a_reference_that_is_not_a_number():
     p.ref[0, 0] = -1.0
     out = p.call("preference")
     assert torch.isfinite(out["loss"]).all() and torch.isfinite(out["grad_logits"]).all()
+
+
+@pytest.mark.parametrize("V", [39, 1500, 5000, 40000, 140001])
+def test_ratios_far_from_one(V):
+    """Log-ratios beyond float32's exponentials: an advantage of 0 has no loss
+    and no gradient, one that the clip holds the clip's loss, and a small one a
+    finite product, as in 64 bits.  r A = e^D A with D known to E (logp's
+    error): relative error E, and its rounding (by 2^-149 where the value is
+    smaller than float32 holds)."""
+    from semi_markov_crf_b200 import semicrf
+    B, T = 6, 2
+    x = _scores(B, T, V, torch.float32, V)
+    p = Problem(x, [T] * B, seed=V)
+    gap = torch.tensor([100.0, 500.0, 100.0, 95.0, -120.0, 80.0], device="cuda")[:, None]
+    old = (p.logp - gap).float()
+    adv = torch.tensor([0.0, 0.0, 1.0, -1e-20, 1.0, -1e-3], device="cuda")
+    for hi in (0.3, math.inf):
+        out = semicrf.policy_loss(x, p.lengths, p.y, old, adv, clip_low=0.2, clip_high=hi)
+        r, A = (p.logp - old.double()).exp(), adv.double()[:, None]
+        free, cut = r * A, r.clamp(0.8, 1 + hi) * A
+        want = -torch.minimum(free, cut)
+        if hi < math.inf:
+            _near("loss", out["loss"].double(), want.sum(1),
+                  (want.abs() * (sum_error(V) + 4 * U)).sum(1) + U * want.sum(1).abs() + 2.0 ** -149)
+        else:
+            keep = [0, 1, 3, 4, 5]   # e^100 is no float32
+            _near("loss", out["loss"].double()[keep], want.sum(1)[keep],
+                  ((want.abs() * (sum_error(V) + 4 * U)).sum(1) + U * want.sum(1).abs()
+                   + 2.0 ** -149)[keep])
+            assert out["loss"][2].item() == -math.inf
+        held = cut < free
+        assert torch.equal(out["clipped"], held.sum(1).int())
+        slope = torch.where(held, torch.zeros_like(r), -free)
+        q = p.logq.exp()
+        hot = torch.zeros_like(q).scatter_(2, p.at(), 1.0)
+        for b in (0, 1, 3, 4, 5) + ((2,) if hi < math.inf else ()):
+            a = slope[b][:, None]
+            w = a * (hot[b] - q[b])
+            tol = a.abs() * (q[b] * (E2(V) + 2 * U * p.gap[b]) + hot[b] * E2(V)) + U * w.abs()
+            _near(f"gradient {b}", out["grad_logits"][b], w, tol + 2.0 ** -120)
+
+
+def E2(V):
+    """A gradient entry's error relative to its softmax, its factor's with it."""
+    return 2 * sum_error(V) + 24 * U
+
+
+def test_path_ratios_far_from_one():
+    """The same in float64, on paths."""
+    from semi_markov_crf_b200 import semicrf
+    t = lambda *v: torch.tensor(v, dtype=torch.float64).cuda()
+    logp = t(-10.0, -10.0, -10.0, -10.0)
+    old = t(-900.0, -900.0, -900.0, 900.0)
+    out = semicrf.policy_scores(logp, old, t(0.0, 1.0, -0.0, 0.0))
+    assert out["loss"].tolist() == [0.0, -1.2, 0.0, 0.0]
+    assert out["grad_logp"].tolist() == [0.0, 0.0, 0.0, 0.0]
+    out = semicrf.policy_scores(logp, old, t(0.0, 0.0, 0.0, 0.0), clip_high=math.inf)
+    assert out["loss"].tolist() == [0.0] * 4 and out["grad_logp"].tolist() == [0.0] * 4
+    out = semicrf.policy_scores(t(math.nan), t(-1.0), t(0.0))
+    assert math.isnan(out["loss"][0]) and math.isnan(out["grad_logp"][0])
