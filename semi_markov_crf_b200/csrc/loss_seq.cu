@@ -101,7 +101,8 @@ __device__ __forceinline__ void logistic(double u, double smoothing, double& los
   const double below = fmax(-u, 0.0) + l, above = fmax(u, 0.0) + l;  // -log sigma(u), -log sigma(-u)
   const double lesser = t / (1.0 + t), greater = 1.0 / (1.0 + t);
   const double sig = u >= 0.0 ? greater : lesser, gis = u >= 0.0 ? lesser : greater;
-  loss = (1.0 - smoothing) * below + (smoothing > 0.0 ? smoothing * above : 0.0);
+  // either may be infinite, and a weight of 0 leaves it out
+  loss = (smoothing < 1.0 ? (1.0 - smoothing) * below : 0.0) + (smoothing > 0.0 ? smoothing * above : 0.0);
   slope = -(1.0 - smoothing) * gis + smoothing * sig;
   if (u != u) loss = slope = u;
 }

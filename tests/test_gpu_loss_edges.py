@@ -426,3 +426,24 @@ def test_path_ratios_far_from_one():
     assert out["loss"].tolist() == [0.0] * 4 and out["grad_logp"].tolist() == [0.0] * 4
     out = semicrf.policy_scores(t(math.nan), t(-1.0), t(0.0))
     assert math.isnan(out["loss"][0]) and math.isnan(out["grad_logp"][0])
+
+
+def test_preferences_of_impossible_labels():
+    """A labelling of probability zero: u = -inf, where a smoothing of 1 leaves
+    -log sigma(-u) = 0 alone, and u = +inf, where a smoothing of 0 leaves
+    -log sigma(u) = 0; nothing is multiplied by a weight of 0."""
+    from semi_markov_crf_b200 import semicrf
+    inf = math.inf
+    c = torch.tensor([-inf, inf, -inf, inf, -inf, inf], dtype=torch.float64).cuda()
+    r = torch.zeros(6, dtype=torch.float64).cuda()
+    for smoothing, loss, grad in ((1.0, [0.0, inf], [0.0, 1.0]), (0.0, [inf, 0.0], [-1.0, 0.0]),
+                                  (0.5, [inf, inf], [-0.5, 0.5])):
+        out = semicrf.preference_scores(c, r, beta=1.0, smoothing=smoothing)
+        assert out["loss"].tolist() == loss * 3, smoothing
+        assert out["grad_chosen"].tolist() == grad * 3, smoothing
+    x = torch.zeros(2, 1, 10, device="cuda")
+    x[0, 0, 3] = -inf
+    n = torch.ones(2, dtype=torch.int32, device="cuda")
+    y = torch.full((2, 1), 3, dtype=torch.int32, device="cuda")
+    out = semicrf.preference_loss(x, n, y, beta=1.0, smoothing=1.0)
+    assert out["loss"].tolist() == [0.0] and not bool(out["grad_logits"].any())
