@@ -521,6 +521,18 @@ SEMICRF_API int semicrf_selftest_bounded_wait(void *ws, size_t ws_bytes, int spi
 SEMICRF_API int semicrf_selftest_bounds(void *ws, size_t ws_bytes, semicrf_stream_t stream);
 
 /*
+ * Self-test of the bounded waits of the label-score losses' rings, in the
+ * bounds-checking build (no counterpart on the pages).  With spins > 0, in the
+ * calls that follow the warp that joins a row's parts gives up before its first
+ * row, in the last CTA of each cluster, and every wait that then lacks something
+ * gives up after `spins` polls: a call over rows that stream through rings ends
+ * with SEMICRF_ERR_DEVICE_TIMEOUT in its status word and with outputs of no
+ * meaning.  0 ends the self-test.  The release build returns
+ * SEMICRF_ERR_UNSUPPORTED.
+ */
+SEMICRF_API int semicrf_selftest_ring_stall(int spins);
+
+/*
  * Diagnostic timing (no counterpart on the pages).  semicrf_profile_enable(1)
  * clears the record and starts bracketing every kernel this library launches
  * with two CUDA events on the launch stream; semicrf_profile_enable(0) stops.

@@ -143,6 +143,14 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
+// Its halves, where no memory is to be ordered (a release would wait for the
+// thread's stores): a thread that has arrived may go on, and end.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // Plain store of one float into the shared memory of CTA `rank` of this
 // cluster, at the offset `local` has in this CTA's shared memory (the same

@@ -102,6 +102,7 @@ inline cudaError_t launch_loss_rows(int mode, int type, const RowArgs& a, cudaSt
                         : type == LT_BF16 ? launch_rows_bf16(mode, a, st) : launch_rows_f16(mode, a, st);
 }
 int loss_sm_count();  // of the current device
+int loss_ring_stall();  // semicrf_selftest_ring_stall's polls (bounds-checking build)
 
 // A launch that may be set up while the kernel before it in the stream ends:
 // the kernel calls after_previous() before it touches anything.

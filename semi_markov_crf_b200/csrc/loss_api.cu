@@ -1,5 +1,6 @@
 // loss_api.cu -- the C ABI of the training losses over label scores
 // (semicrf.h): argument checks, workspace layout and launches.  Host code only.
+#include <atomic>
 #include <cmath>
 
 #include "loss.cuh"
@@ -147,6 +148,11 @@ int loss_sm_count() {
   return v;
 }
 
+namespace {
+std::atomic<int> ring_stall{0};
+}
+int loss_ring_stall() { return ring_stall.load(std::memory_order_relaxed); }
+
 }  // namespace semicrf
 
 using namespace semicrf;
@@ -157,6 +163,16 @@ extern "C" int semicrf_loss_workspace_bytes(int B, int T, size_t* bytes) {
   if (rc) return rc;
   *bytes = loss_layout(B, T, nullptr, nullptr);
   return SEMICRF_OK;
+}
+
+extern "C" int semicrf_selftest_ring_stall(int spins) {
+  if (spins < 0) return SEMICRF_ERR_INVALID_ARG;
+#ifdef SEMICRF_BOUNDS_CHECK
+  ring_stall.store(spins, std::memory_order_relaxed);
+  return SEMICRF_OK;
+#else
+  return SEMICRF_ERR_UNSUPPORTED;  // the release build's rings do not stall on request
+#endif
 }
 
 extern "C" int semicrf_label_logprob(const void* logits, int dtype, int64_t ld,

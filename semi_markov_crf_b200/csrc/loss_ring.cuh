@@ -35,13 +35,20 @@
 //
 // Every wait is bounded: one that gives up records ST_DEVICE_TIMEOUT in the
 // status word, and its thread runs on without waiting (every access stays
-// within the rows and the rings), so that the kernel ends.
+// within the rows and the rings), so that the kernel ends.  It passes nothing on
+// any more, neither to the barriers of its CTA (a chunk given back twice would be
+// filled twice at once) nor to the other CTAs of its cluster, so that their waits
+// give up in turn; and a CTA to which others may still send ends last.
 
 constexpr int RING_WARPS = 16;                      // reducers and writers of a CTA
 constexpr int RING_GROUPS = 8;                      // at most
 constexpr int RING_GROUPS_DISTILL = 4;              // at most, with its teacher warps:
 constexpr int TEACHERS_MAX = 3;
 __host__ __device__ constexpr int teacher_warps(int groups) { return groups == 4 ? 2 : TEACHERS_MAX; }
+// A teacher warp that skips a row's `written` phase knows it closed before it looks at
+// the next: its next row's note means that the note two rows before is free again.
+static_assert(teacher_warps(1) >= 2 && teacher_warps(2) >= 2 && teacher_warps(4) >= 2,
+              "a teacher warp takes at most every second row");
 template <int MODE>
 constexpr int ring_threads =  // at most
     (RING_WARPS + 1 +
@@ -57,6 +64,9 @@ struct RingShape {
   int W;      // warps of a group
   int slots;  // chunks of a group's ring
   int cl;     // CTAs that share a row
+#ifdef SEMICRF_BOUNDS_CHECK
+  int stall;  // semicrf_selftest_ring_stall; 0: none
+#endif
 };
 
 // What the scalar warp tells the writers about a row.
@@ -108,14 +118,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// This warp is done with a chunk.  Its reads are ordinary accesses and the copy
-// that follows is an asynchronous one: without the fence between the two the
-// copy may overtake reads that are still under way.
-__device__ __forceinline__ void give_back(uint64_t* empty, int lane) {
-  fence_proxy_async();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(empty);
-}
 
 // A position in a group's ring.
 struct Cursor {
@@ -139,18 +141,31 @@ struct Turn {
   }
 };
 
-// Waits that give up once and for all.
+// A thread's waits and arrivals, which end once and for all when one wait gives up.
 struct Waiter {
   int* status;
+  int spins;
   bool dead;
   __device__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (!dead && !mbar_wait(bar, parity, WAIT_SPIN_LIMIT)) give_up();
+    if (!dead && !mbar_wait(bar, parity, spins)) give_up();
   }
   __device__ void give_up() {
     dead = true;
     if (status) set_status(status, ST_DEVICE_TIMEOUT);
   }
+  __device__ void arrive(uint64_t* bar) const {
+    if (!dead) mbar_arrive(bar);
+  }
 };
+
+// This warp is done with a chunk.  Its reads are ordinary accesses and the copy
+// that follows is an asynchronous one: without the fence between the two the
+// copy may overtake reads that are still under way.
+__device__ __forceinline__ void give_back(const Waiter& wait, uint64_t* empty, int lane) {
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) wait.arrive(empty);
+}
 
 // The vectors of row x that CTA `rank` of `cl` takes.
 struct Part {
@@ -244,6 +259,7 @@ struct RingPlace {
   int first, units, rows;  // this group's rows: first, first + units, ...
   int rank, cl, slots, chunk_bytes;
   int teachers;  // warps
+  int spins;     // polls before a wait gives up
 };
 
 // ---------------------------------------------------------------------- copier
@@ -295,7 +311,7 @@ __device__ __forceinline__ void ring_copier(const RowArgs& a, unsigned char* rin
       idle = 0;
     } else {
       __nanosleep(100);
-      if (++idle >= WAIT_SPIN_LIMIT) {
+      if (++idle >= pl.spins) {
         if (lane == 0 && a.status) set_status(a.status, ST_DEVICE_TIMEOUT);
         break;
       }
@@ -315,7 +331,7 @@ template <typename T, int MODE, bool RELEASE>
 __device__ __forceinline__ void ring_reduce(const RowArgs& a, const RingPlace& pl, int gt, int GT) {
   GroupState& st = *pl.st;
   const int lane = gt & 31, gw = gt >> 5, chunk_vecs = pl.chunk_bytes / 16;
-  Waiter wait{a.status, false};
+  Waiter wait{a.status, pl.spins, false};
   Cursor cur{0, 0};
   Turn turn{0, 0};
   HeadStream<MODE> heads{};
@@ -350,7 +366,7 @@ __device__ __forceinline__ void ring_reduce(const RowArgs& a, const RingPlace& p
       }
       float sum, odd;
       halves(add2(sum2[0], sum2[1]), sum, odd);
-      if (RELEASE) give_back(&st.empty[cur.slot], lane);
+      if (RELEASE) give_back(wait, &st.empty[cur.slot], lane);
       cur.next(pl.slots);
       s = (mb == NEG_INF && s == 0.0f ? 0.0f : s * ex2(mb - nb)) + (sum + odd);
       mb = nb;
@@ -359,7 +375,7 @@ __device__ __forceinline__ void ring_reduce(const RowArgs& a, const RingPlace& p
     wait(&st.red_free[turn.i], turn.phase ^ 1);
     if (lane == 0) {
       st.red[turn.i][gw] = make_float2(mb, s);
-      mbar_arrive(&st.red_full[turn.i]);
+      wait.arrive(&st.red_full[turn.i]);
     }
     turn.next();
   }
@@ -371,7 +387,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
   constexpr int VE = vec_of<T>;
   GroupState& st = *pl.st;
   const int lane = gt & 31, chunk_vecs = pl.chunk_bytes / 16;
-  Waiter wait{a.status, false};
+  Waiter wait{a.status, pl.spins, false};
   Cursor cur{0, 0};
   Turn turn{0, 0};
   Cursor teacher{0, 0};
@@ -407,7 +423,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
             reinterpret_cast<const uint4*>(pl.ring + (size_t)cur.slot * pl.chunk_bytes);
         const int have = p.n - c;
         if (MODE == LM_DISTILL && note.kind == NOTE_ZERO) {  // read, but its teacher's entries leave nothing
-          give_back(&st.empty[cur.slot], lane);
+          give_back(wait, &st.empty[cur.slot], lane);
           clear(c, min(have, chunk_vecs));
         } else if (plain) {
           uint4 raw[RING_NV];
@@ -421,7 +437,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
               v[e] = mul2(ex2_2(fma2(v[e], sl2, at2)), scale2);
             raw[i] = Vec<T>::pack(v);
           }
-          give_back(&st.empty[cur.slot], lane);
+          give_back(wait, &st.empty[cur.slot], lane);
           uint4* out = reinterpret_cast<uint4*>(gb) + c + gt;
           if (have >= chunk_vecs) {
 #pragma unroll
@@ -446,7 +462,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
               to[e] = from_f32<T>(gv);
             }
           }
-          give_back(&st.empty[cur.slot], lane);
+          give_back(wait, &st.empty[cur.slot], lane);
         }
         cur.next(pl.slots);
       }
@@ -459,8 +475,8 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
     }
     __syncwarp();
     if (lane == 0) {
-      if (MODE == LM_DISTILL) mbar_arrive(&st.written[teacher.slot]);
-      mbar_arrive(&st.note_free[turn.i]);
+      if (MODE == LM_DISTILL) wait.arrive(&st.written[teacher.slot]);
+      wait.arrive(&st.note_free[turn.i]);
     }
     if (MODE == LM_DISTILL) teacher.next(pl.teachers);
     turn.next();
@@ -468,12 +484,15 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
 }
 
 // ----------------------------------------------------------------- scalar warp
+// Returns whether a wait gave up; `stall`: as if one had from the start.
 template <typename T, int MODE, bool GRAD>
-__device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& pl, int warps, int lane) {
+__device__ __forceinline__ bool ring_scalar(const RowArgs& a, const RingPlace& pl, int warps, int lane,
+                                            bool stall) {
   constexpr bool PASS1 = MODE != LM_SCALED;
   constexpr bool NOTES = GRAD || MODE == LM_DISTILL;
   GroupState& st = *pl.st;
-  Waiter wait{a.status, false};
+  Waiter wait{a.status, pl.spins, false};
+  if (stall) wait.give_up();
   Turn turn{0, 0}, rows_read{0, 0};
   Cursor teacher{0, 0};
   HeadStream<MODE> heads{};
@@ -483,8 +502,8 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
     __syncwarp();
     if (lane == 0) {
       st.note[turn.i] = note;
-      mbar_arrive(&st.note_full[turn.i]);
-      if (MODE == LM_DISTILL) mbar_arrive(&st.told[teacher.slot]);
+      wait.arrive(&st.note_full[turn.i]);
+      if (MODE == LM_DISTILL) wait.arrive(&st.told[teacher.slot]);
     }
   };
   for (int i = pl.first; i < pl.rows; i += pl.units) {
@@ -521,7 +540,7 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
           s = v.y;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&st.red_free[rows_read.i]);
+        if (lane == 0) wait.arrive(&st.red_free[rows_read.i]);
         if (ei >= 0) {
           const float xv = to_f32<T>(xe), eb = xv * a.sl;
           join_pair(mb, s, eb, eb < -BASE_MAX ? 0.0f : ex2(fmaf(xv, a.sl, -eb)));
@@ -531,13 +550,13 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
           // two barriers and two sets of slots, so that a peer's next row cannot
           // meet this one's
           uint64_t* bar = &st.peer[rows_read.i];
-          if (lane == 0) mbar_expect_tx(bar, 8 * pl.cl);
+          if (lane == 0 && !wait.dead) mbar_expect_tx(bar, 8 * pl.cl);
           __syncwarp();
-          if (lane < pl.cl) {
+          if (lane < pl.cl && !wait.dead) {
             st_async_cluster(&st.part[rows_read.i][pl.rank].x, bar, lane, mb);
             st_async_cluster(&st.part[rows_read.i][pl.rank].y, bar, lane, s);
           }
-          if (!wait.dead && !mbar_wait_cluster(bar, rows_read.phase, WAIT_SPIN_LIMIT)) wait.give_up();
+          if (!wait.dead && !mbar_wait_cluster(bar, rows_read.phase, pl.spins)) wait.give_up();
           mb = NEG_INF;
           s = 0.0f;
           if (lane < pl.cl) {
@@ -602,12 +621,13 @@ __device__ __forceinline__ void ring_scalar(const RowArgs& a, const RingPlace& p
       if (blank) publish(note);
       if (MODE == LM_DISTILL) {
         __syncwarp();  // the edges are written: the teacher warp may change them
-        if (GRAD && lane == 0) mbar_arrive(&st.written[teacher.slot]);
+        if (GRAD && lane == 0) wait.arrive(&st.written[teacher.slot]);
         teacher.next(pl.teachers);
       }
       turn.next();
     }
   }
+  return wait.dead;
 }
 
 // --------------------------------------------------------------- teacher warps
@@ -620,7 +640,7 @@ __device__ __forceinline__ void ring_teacher(const RowArgs& a, const RingPlace& 
                                              int me, int lane) {
   constexpr int VE = vec_of<T>;
   GroupState& st = *pl.st;
-  Waiter wait{a.status, false};
+  Waiter wait{a.status, pl.spins, false};
   const int step = pl.units * pl.teachers;
   const Teacher tc{entries, reinterpret_cast<int*>(entries + a.k), entries + 2 * a.k,
                    entries + 3 * a.k, reinterpret_cast<int*>(entries + TEACHER_WORDS * a.k)};
@@ -653,14 +673,14 @@ __device__ __forceinline__ void ring_teacher(const RowArgs& a, const RingPlace& 
     __syncwarp();  // (accumulation: all have read the values that the writers will change)
     if (lane == 0) {
       st.teacher[me] = TeacherNote{th.P, th.malformed || th.none};
-      mbar_arrive(&st.teacher_full[me]);
+      wait.arrive(&st.teacher_full[me]);
     }
     own ^= 1;
     const int i = n & 1;
     wait(&st.told[me], own);
     const RowNote note = st.note[i];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&st.note_free[i]);
+    if (lane == 0) wait.arrive(&st.note_free[i]);
     if (blank) continue;
     if (th.malformed || th.none) {
       if (lane == 0 && pl.rank == 0) blank_outputs<LM_DISTILL>(a, r, th.malformed);
@@ -692,6 +712,13 @@ __global__ void __launch_bounds__(ring_threads<MODE>, 1)
   pl.rank = pl.cl > 1 ? (int)cluster_ctarank() : 0;
   pl.rows = a.B * a.T;  // <= 2^27
   pl.units = (int)(gridDim.x / pl.cl) * groups;
+#ifdef SEMICRF_BOUNDS_CHECK
+  pl.spins = shape.stall ? shape.stall : WAIT_SPIN_LIMIT;
+  const bool stall = shape.stall && pl.rank == pl.cl - 1;
+#else
+  pl.spins = WAIT_SPIN_LIMIT;
+  constexpr bool stall = false;
+#endif
   const size_t ring_bytes = (size_t)pl.slots * pl.chunk_bytes;
   GroupState* states = reinterpret_cast<GroupState*>(ring_smem + groups * ring_bytes);
   float* entries = reinterpret_cast<float*>(states + groups);
@@ -724,20 +751,19 @@ __global__ void __launch_bounds__(ring_threads<MODE>, 1)
   if (pl.cl > 1) cluster_sync();
   if (MODE == LM_SCALED) after_previous();
 
-  if (warp == RING_WARPS + groups) {
-    pl.first = first;
-    ring_copier<T, MODE>(a, ring_smem, states, groups, ring_bytes, pl, lane);
-    return;
-  }
   const int teacher = warp - (RING_WARPS + groups + 1);
   const int gi = warp < RING_WARPS ? warp / W : teacher < 0 ? warp - RING_WARPS : teacher / pl.teachers;
   pl.first = first + gi;
   pl.ring = ring_smem + gi * ring_bytes;
   pl.st = states + gi;
-  if (MODE == LM_DISTILL && teacher >= 0) {
+  bool gave_up = false;
+  if (warp == RING_WARPS + groups) {
+    pl.first = first;
+    ring_copier<T, MODE>(a, ring_smem, states, groups, ring_bytes, pl, lane);
+  } else if (MODE == LM_DISTILL && teacher >= 0) {
     ring_teacher<T, GRAD>(a, pl, entries + teacher * teacher_entry(a.k, a.V), teacher % pl.teachers, lane);
   } else if (warp >= RING_WARPS) {
-    ring_scalar<T, MODE, GRAD>(a, pl, role_warps, lane);
+    gave_up = ring_scalar<T, MODE, GRAD>(a, pl, role_warps, lane, stall);
   } else {
     const int gw = warp - gi * W;
     if (BOTH) {
@@ -747,6 +773,17 @@ __global__ void __launch_bounds__(ring_threads<MODE>, 1)
       ring_reduce<T, MODE, true>(a, pl, gw * 32 + lane, role_warps * 32);
     } else {
       ring_write<T, MODE>(a, pl, gw * 32 + lane, role_warps * 32);
+    }
+  }
+  if (PASS1 && pl.cl > 1) {
+    // A CTA that has had its peers' pairs of all rows may end, for they send no
+    // more.  One that has not keeps its shared memory until every thread of the
+    // cluster is through, and then until what they sent last has come.
+    __syncwarp();
+    cluster_arrive();
+    if (__any_sync(FULL_MASK, gave_up)) {
+      cluster_wait();
+      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
   }
 }
@@ -810,6 +847,9 @@ bool launch_ring(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   // Warps a group: 8 KB of a row for each (rows in flight hide one another's
   // latency), all 16 where there are too few rows for more groups.
   RingShape s;
+#ifdef SEMICRF_BOUNDS_CHECK
+  s.stall = loss_ring_stall();
+#endif
   s.W = MODE == LM_DISTILL ? RING_WARPS / RING_GROUPS_DISTILL : 2;
   while (s.W < RING_WARPS &&
          (row > (size_t)s.W * 8 * 1024 || rows <= (long long)sms * (RING_WARPS / s.W) / 2 ||

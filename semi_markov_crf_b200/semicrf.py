@@ -16,7 +16,7 @@ import torch
 __all__ = ["workspace_bytes", "workspace_itemize", "WS_GROUPS", "launch_shape", "prefix_center", "forward", "backward", "viterbi", "path_score",
            "get_status", "FLAG_NEGATE_GRAD",
            "strerror", "SemiCRFError", "library_path", "Workspace", "FLAG_NO_CENTER",
-           "FLAG_FORWARD_ONLY", "FLAG_LOG_DOMAIN", "selftest_bounded_wait", "selftest_bounds", "ring_domains", "profile_enable", "profile_read",
+           "FLAG_FORWARD_ONLY", "FLAG_LOG_DOMAIN", "selftest_bounded_wait", "selftest_bounds", "selftest_ring_stall", "ring_domains", "profile_enable", "profile_read",
            "forward_noalloc", "NOALLOC_SCRATCH_BYTES",
            "FLAG_ACCUMULATE", "FLAG_AVERAGE", "LossWorkspace", "loss_workspace_bytes",
            "label_logprob", "policy_loss", "preference_loss", "distill_loss", "policy_scores",
@@ -96,6 +96,7 @@ lib.semicrf_source_digest.argtypes = []
 lib.semicrf_source_digest.restype = ctypes.c_char_p
 lib.semicrf_selftest_bounded_wait.argtypes = [_vp, _sz, _i, _vp]
 lib.semicrf_selftest_bounds.argtypes = [_vp, _sz, _vp]
+lib.semicrf_selftest_ring_stall.argtypes = [_i]
 lib.semicrf_forward_noalloc.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _u, _vp, _vp]
 lib.semicrf_ring_domains.argtypes = [_vp, _sz, _i, _i, _i, _i, _u, _vp, ctypes.POINTER(ctypes.c_int32)]
 lib.semicrf_profile_enable.argtypes = [_i]
@@ -106,7 +107,8 @@ for _f in ("semicrf_backward_segments", "semicrf_launch_shape", "semicrf_workspa
            "semicrf_path_score_proj", "semicrf_loss_workspace_bytes", "semicrf_label_logprob",
            "semicrf_policy_loss", "semicrf_preference_loss", "semicrf_distill_loss",
            "semicrf_policy_scores", "semicrf_preference_scores",
-           "semicrf_selftest_bounded_wait", "semicrf_selftest_bounds", "semicrf_ring_domains"):
+           "semicrf_selftest_bounded_wait", "semicrf_selftest_bounds", "semicrf_selftest_ring_stall",
+           "semicrf_ring_domains"):
     getattr(lib, _f).restype = _i
 
 
@@ -745,6 +747,14 @@ def selftest_bounds(ws: Workspace) -> int:
     _check(lib.semicrf_get_status(ws.ptr, _stream(ws.buf.device), ctypes.byref(st)),
            "semicrf_get_status")
     return int(st.value)
+
+
+def selftest_ring_stall(spins: int):
+    """Bounds-checking build: with spins > 0 the rings of the label-score losses
+    stall in the calls that follow, and their waits give up after `spins` polls
+    (status SEMICRF_ERR_DEVICE_TIMEOUT); 0 ends that.  The release build raises
+    SemiCRFError(SEMICRF_ERR_UNSUPPORTED)."""
+    _check(lib.semicrf_selftest_ring_stall(int(spins)), "semicrf_selftest_ring_stall")
 
 
 def profile_enable(on: bool = True):
