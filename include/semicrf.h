@@ -344,7 +344,7 @@ SEMICRF_API int semicrf_path_score_proj(const float *em, const int32_t *lengths,
  *                 logits + (b * T + t) * ld elements (ld >= V).
  *  - grad_logits  rows of the same type, grad_ld apart; every row is written
  *                 (zeros where a position does not count), or added to under
- *                 SEMICRF_FLAG_ACCUMULATE.  Must not overlap logits.
+ *                 SEMICRF_FLAG_ACCUMULATE.
  *  - lengths [B], labels [B, T] int32: position (b, t) counts when
  *                 t < lengths[b] and labels[b, t] >= 0.  Scores and other
  *                 per-position inputs of positions that do not count are never
@@ -357,7 +357,8 @@ SEMICRF_API int semicrf_path_score_proj(const float *em, const int32_t *lengths,
  *                 written by every call (semicrf_get_status): a length outside
  *                 [0, T] gives SEMICRF_ERR_BAD_LENGTH, NaN sums and no gradient
  *                 for that sequence.
- *  - Output pointers other than the workspace may be NULL where marked.
+ *  - Output pointers other than the workspace may be NULL where marked.  No
+ *                 output may overlap an input (SEMICRF_ERR_INVALID_ARG).
  *  - Limits: V <= 2^24, B * T <= 2^27, k <= 1024 (SEMICRF_ERR_UNSUPPORTED).
  *  - A row holding NaN or +inf, or nothing but -inf, has no softmax: its terms
  *    and its gradient row are NaN.  -inf beside finite scores is a label of
@@ -457,7 +458,8 @@ SEMICRF_API int semicrf_distill_loss(const void *logits, int dtype, int64_t ld,
  * semicrf_path_score write them.  The gradients are float64 and are what
  * semicrf_path_score takes as grad_score and semicrf_backward, negated, as
  * grad_logZ.  Formulas as above with one ratio per path; grad_loss [N] nullable,
- * outputs nullable.  ref_chosen and ref_rejected are given together or not at all.
+ * outputs nullable, none overlapping an input.  ref_chosen and ref_rejected are
+ * given together or not at all.
  */
 SEMICRF_API int semicrf_policy_scores(const double *logp, const double *old_logp,
                                       const double *ref_logp, const double *adv, int N,

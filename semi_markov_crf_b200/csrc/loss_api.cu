@@ -2,6 +2,7 @@
 // (semicrf.h): argument checks, workspace layout and launches.  Host code only.
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 
 #include "loss.cuh"
 #include "semicrf.h"
@@ -45,6 +46,28 @@ int check_sizes(int B, int T) {
 
 bool is_finite(double v) { return std::isfinite(v); }
 
+// An array of a call; a null one overlaps nothing.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// A row's inputs are read by several warps and CTAs, one of which writes its
+// outputs: an output in an input's place would change what the others read.
+bool overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (const Span& o : outputs)
+    for (const Span& i : inputs) {
+      const uintptr_t po = (uintptr_t)o.p, pi = (uintptr_t)i.p;
+      if (po && pi && po < pi + i.bytes && pi < po + o.bytes) return true;
+    }
+  return false;
+}
+
+size_t row_bytes(const RowArgs& a, int dtype, int64_t ld) {
+  const size_t rows = (size_t)a.B * a.T, es = dtype == SEMICRF_F32 ? 4 : 2;
+  return rows ? ((rows - 1) * (size_t)ld + a.V) * es : 0;
+}
+
 // The checks every logits form shares, and the arguments they fill.
 int prepare_rows(const void* logits, int dtype, int64_t ld, const int32_t* lengths, int B, int T,
                  int V, double temperature, unsigned flags, unsigned known, void* ws,
@@ -65,12 +88,6 @@ int prepare_rows(const void* logits, int dtype, int64_t ld, const int32_t* lengt
   if ((uintptr_t)logits % es || (uintptr_t)grad_logits % es) return SEMICRF_ERR_INVALID_ARG;
   if ((flags & SEMICRF_FLAG_ACCUMULATE) && dtype != SEMICRF_F32) return SEMICRF_ERR_INVALID_ARG;
   if (ws_bytes < loss_layout(B, T, nullptr, nullptr)) return SEMICRF_ERR_WORKSPACE_TOO_SMALL;
-  if (rows > 0 && grad_logits) {  // the row is read again while its gradient is written
-    const uintptr_t x0 = (uintptr_t)logits, g0 = (uintptr_t)grad_logits;
-    const uintptr_t x1 = x0 + ((uintptr_t)(rows - 1) * (uintptr_t)ld + V) * es;
-    const uintptr_t g1 = g0 + ((uintptr_t)(rows - 1) * (uintptr_t)grad_ld + V) * es;
-    if (x0 < g1 && g0 < x1) return SEMICRF_ERR_INVALID_ARG;
-  }
   loss_layout(B, T, ws, &p);
   a = RowArgs{};
   a.x = logits;
@@ -189,6 +206,10 @@ extern "C" int semicrf_label_logprob(const void* logits, int dtype, int64_t ld,
   if ((long long)B * T > 0 && !labels) return SEMICRF_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (B == 0) return empty_batch(p, st);
+  const size_t n = (size_t)B * T * 4;
+  if (overlap({{logp, n}, {score, (size_t)B * 4}, {grad_logits, row_bytes(a, dtype, grad_ld)}},
+              {{logits, row_bytes(a, dtype, ld)}, {lengths, (size_t)B * 4}, {labels, n}, {grad_logp, n}}))
+    return SEMICRF_ERR_INVALID_ARG;
   a.labels = labels;
   a.grad_logp = grad_logp;
   a.logp = logp;
@@ -214,6 +235,11 @@ extern "C" int semicrf_policy_loss(const void* logits, int dtype, int64_t ld,
   if ((long long)B * T > 0 && (!labels || !old_logp || !adv)) return SEMICRF_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (B == 0) return empty_batch(p, st);
+  const size_t n = (size_t)B * T * 4, nb = (size_t)B * 4;
+  if (overlap({{logp, n}, {loss, nb}, {kl, nb}, {clipped, nb}, {grad_logits, row_bytes(a, dtype, grad_ld)}},
+              {{logits, row_bytes(a, dtype, ld)}, {lengths, nb}, {labels, n}, {old_logp, n}, {ref_logp, n},
+               {adv, adv_per_token ? n : nb}, {grad_loss, 2 * nb}}))
+    return SEMICRF_ERR_INVALID_ARG;
   a.labels = labels;
   a.old_logp = old_logp;
   a.ref_logp = ref_logp;
@@ -250,6 +276,10 @@ extern "C" int semicrf_preference_loss(const void* logits, int dtype, int64_t ld
   if ((long long)B * T > 0 && !labels) return SEMICRF_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (B == 0) return empty_batch(p, st);
+  const size_t n = (size_t)B * T * 4, nb = (size_t)B * 4;
+  if (overlap({{logp, n}, {loss, nb / 2}, {reward, nb}, {grad_logits, row_bytes(a, dtype, grad_ld)}},
+              {{logits, row_bytes(a, dtype, ld)}, {lengths, nb}, {labels, n}, {ref_logp, n}, {grad_loss, nb}}))
+    return SEMICRF_ERR_INVALID_ARG;
   a.labels = labels;
   a.ref_logp = ref_logp;
   a.logp = logp;
@@ -300,6 +330,11 @@ extern "C" int semicrf_distill_loss(const void* logits, int dtype, int64_t ld,
   if ((long long)B * T > 0 && (!teacher_ids || !teacher_logits)) return SEMICRF_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (B == 0) return empty_batch(p, st);
+  const size_t n = (size_t)B * T * 4, nb = (size_t)B * 4;
+  if (overlap({{token_loss, n}, {loss, nb}, {grad_logits, row_bytes(a, dtype, grad_ld)}},
+              {{logits, row_bytes(a, dtype, ld)}, {lengths, nb}, {teacher_ids, n * k},
+               {teacher_logits, n * k}, {teacher_lse, n}, {grad_loss, 2 * nb}}))
+    return SEMICRF_ERR_INVALID_ARG;
   a.ids = teacher_ids;
   a.tl = teacher_logits;
   a.tlse = teacher_lse;
@@ -317,6 +352,10 @@ extern "C" int semicrf_policy_scores(const double* logp, const double* old_logp,
   if (N < 0 || !clip_ok(clip_low, clip_high, kl_coef)) return SEMICRF_ERR_INVALID_ARG;
   if (N == 0) return SEMICRF_OK;
   if (!logp || !old_logp || !adv) return SEMICRF_ERR_INVALID_ARG;
+  const size_t n = (size_t)N * 8;
+  if (overlap({{loss, n}, {kl, n}, {grad_logp, n}},
+              {{logp, n}, {old_logp, n}, {ref_logp, n}, {adv, n}, {grad_loss, n}}))
+    return SEMICRF_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   LaunchTimer lt("policy_scores_kernel", st);
   return launch_policy_scores(logp, old_logp, ref_logp, adv, N, 1.0 - clip_low, 1.0 + clip_high,
@@ -336,6 +375,10 @@ extern "C" int semicrf_preference_scores(const double* chosen, const double* rej
   if ((ref_chosen == nullptr) != (ref_rejected == nullptr)) return SEMICRF_ERR_INVALID_ARG;
   if (N == 0) return SEMICRF_OK;
   if (!chosen || !rejected) return SEMICRF_ERR_INVALID_ARG;
+  const size_t n = (size_t)N * 8;
+  if (overlap({{loss, n}, {grad_chosen, n}, {grad_rejected, n}},
+              {{chosen, n}, {rejected, n}, {ref_chosen, n}, {ref_rejected, n}, {grad_loss, n}}))
+    return SEMICRF_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   LaunchTimer lt("preference_scores_kernel", st);
   return launch_preference_scores(chosen, rejected, ref_chosen, ref_rejected, N, beta, margin,
