@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(L, 640 / L)
   start_status(a);
   const Head h = make_head<MODE>(a, load_head<MODE>(a, r));
   const T* x = row_at<T>(a.x, r, a.ldx);
-  T* g = a.g && MODE != LM_PREFERENCE ? row_at<T>(a.g, r, a.ldg) : nullptr;
+  T* g = a.g ? row_at<T>(a.g, r, a.ldg) : nullptr;
   const Split sp = split_row(x, V);
   const int ei = tid < sp.edge ? edge_index<T>(sp, tid) : -1;
   auto fill_zero = [&]() {
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(L, 640 / L)
 template <typename T, int MODE>
 bool launch_cta(const RowArgs& a, cudaStream_t st, cudaError_t& e) {
   const uintptr_t px = reinterpret_cast<uintptr_t>(a.x), pg = reinterpret_cast<uintptr_t>(a.g);
-  const bool grad = a.g != nullptr && MODE != LM_PREFERENCE;
+  const bool grad = a.g != nullptr;
   if (a.V > CTA_V_MAX) return false;
   // without a gradient a ring's warps all reduce: 62 against 68 us at 4096 scores
   if (!grad && MODE != LM_DISTILL) return false;

@@ -5,10 +5,11 @@
 // a batch of sequences).  What counts is instructions a row (the scalar work
 // of a position costs as much as its elements) and rows in flight: few lanes a
 // row, so that a warp works on several at once and a reduction is log2 L
-// shuffles, one row a group, and no more registers than 28 to 40 warps an SM
-// leave.  (Loading a row ahead costs the registers of a third of the warps
-// and was slower: 31 against 21 us for 80000 rows of 128 float32; tiles in
-// shared memory behind TMA copies, 16 warps an SM, took 33.)
+// shuffles, one row a group, and no more registers than 16, 32 or 40 warps an
+// SM leave (64, 32 or up to 16 elements a lane).  (Loading a row ahead costs the
+// registers of a third of the warps and was slower: 31 against 21 us for 80000
+// rows of 128 float32; tiles in shared memory behind TMA copies, 16 warps an SM,
+// took 33.)
 //
 // Layouts: VECTORS, rows on 16-byte boundaries; SPLIT, the 16-byte vectors
 // within a row and up to 14 single elements, one a lane; ELEMENTS, neighbouring
@@ -351,44 +352,49 @@ cudaError_t launch_lanes_shape(const RowArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// NE: 8, 16 or (vectors only) 32 elements a lane.
-template <typename T, int MODE, int L, int LAY, int KEEP>
-cudaError_t launch_lanes_of(const RowArgs& a, cudaStream_t st) {
-  if (a.V <= 8 * L) return launch_lanes_shape<T, MODE, L, 8, LAY, KEEP>(a, st);
-  if (a.V <= 16 * L) return launch_lanes_shape<T, MODE, L, 16, LAY, KEEP>(a, st);
-  if constexpr (LAY != ELEMENTS && L < 32) {
-    if (a.V <= 32 * L) return launch_lanes_shape<T, MODE, L, 32, LAY, KEEP>(a, st);
-    if constexpr (L >= 2 && MODE != LM_SCALED && sizeof(T) == 2) return launch_lanes_shape<T, MODE, L, 64, LAY, KEEP>(a, st);
+// Whether launch_lanes() below ever takes a shape: only those are compiled (308 of
+// the 562 that the ranges of lanes, elements, layouts and kept entries span, for
+// float32 and one 16-bit type).  Rows take the fewest lanes that hold them, more
+// only for a teacher's entries, so that most have half of NE in use at least.
+template <typename T, int MODE>
+constexpr bool lanes_reached(int L, int NE, int LAY, int KEEP) {
+  constexpr bool half = sizeof(T) == 2, read_only = MODE == LM_PREFERENCE;
+  if (L < 32 && NE == 32 && LAY == ELEMENTS) return false;
+  if (L < 32 && NE == 64 && (LAY == ELEMENTS || L == 1 || !half || MODE == LM_SCALED)) return false;
+  if (LAY == SPLIT && L < 16) return false;
+  if (MODE == LM_DISTILL && KEEP == 0) return L == 32 && !(LAY == SPLIT && NE == 8);
+  if (KEEP == 4) {
+    if (LAY == SPLIT) return NE >= (L == 16 ? 32 : 16);
+    return L >= (LAY == ELEMENTS ? 4 : 8);
   }
-  if constexpr (L == 32) {
-    if (a.V <= 32 * L) return launch_lanes_shape<T, MODE, L, 32, LAY, KEEP>(a, st);
-    return launch_lanes_shape<T, MODE, L, 64, LAY, KEEP>(a, st);
-  }
-  return cudaErrorInvalidValue;  // not reached: L is chosen by V
+  if (LAY == ELEMENTS)
+    return L == 1 || (L == 32 ? NE >= 16 && !read_only : NE == 16 || (MODE == LM_DISTILL && L <= 4));
+  if (read_only && half && NE == 32 && L > (LAY == SPLIT ? 16 : 2)) return false;
+  return NE >= 32 || (LAY == VECTORS && (L == 1 || (MODE == LM_DISTILL && L <= 8)));
 }
 
 template <typename T, int MODE, int LAY, int KEEP>
 cudaError_t launch_lanes_with(const RowArgs& a, int L, cudaStream_t st) {
-  if constexpr (LAY == SPLIT) {
-    if (L == 16) return launch_lanes_of<T, MODE, 16, LAY, KEEP>(a, st);
-  }
-  if constexpr (KEEP == 4 && LAY == ELEMENTS) {
-    if (L == 4) return launch_lanes_of<T, MODE, 4, LAY, KEEP>(a, st);
-  }
-  if constexpr (KEEP == 4 && LAY != SPLIT) {  // lists that need four come with 4 or 8 lanes at least
-    if (L == 8) return launch_lanes_of<T, MODE, 8, LAY, KEEP>(a, st);
-    if (L == 16) return launch_lanes_of<T, MODE, 16, LAY, KEEP>(a, st);
-  }
-  if constexpr (KEEP != 4 && LAY != SPLIT) {  // split rows come with 16 or 32
-    switch (L) {
-      case 1: return launch_lanes_of<T, MODE, 1, LAY, KEEP>(a, st);
-      case 2: return launch_lanes_of<T, MODE, 2, LAY, KEEP>(a, st);
-      case 4: return launch_lanes_of<T, MODE, 4, LAY, KEEP>(a, st);
-      case 8: return launch_lanes_of<T, MODE, 8, LAY, KEEP>(a, st);
-      case 16: return launch_lanes_of<T, MODE, 16, LAY, KEEP>(a, st);
-    }
-  }
-  return launch_lanes_of<T, MODE, 32, LAY, KEEP>(a, st);
+  cudaError_t e = cudaErrorInvalidValue;  // stays where the two rules disagree
+  auto shape = [&](auto lanes, auto elements) {
+    constexpr int N = decltype(lanes)::value, NE = decltype(elements)::value;
+    if constexpr (lanes_reached<T, MODE>(N, NE, LAY, KEEP))
+      if (L == N && a.V <= NE * N && (NE == 8 || a.V > NE / 2 * N))
+        e = launch_lanes_shape<T, MODE, N, NE, LAY, KEEP>(a, st);
+  };
+  auto of = [&](auto lanes) {
+    shape(lanes, std::integral_constant<int, 8>{});
+    shape(lanes, std::integral_constant<int, 16>{});
+    shape(lanes, std::integral_constant<int, 32>{});
+    shape(lanes, std::integral_constant<int, 64>{});
+  };
+  of(std::integral_constant<int, 1>{});
+  of(std::integral_constant<int, 2>{});
+  of(std::integral_constant<int, 4>{});
+  of(std::integral_constant<int, 8>{});
+  of(std::integral_constant<int, 16>{});
+  of(std::integral_constant<int, 32>{});
+  return e;
 }
 
 // False where the row is too long for these kernels.

@@ -648,9 +648,13 @@ template <typename T, int MODE>
 cudaError_t rows_in_mode(const RowArgs& a, cudaStream_t st) {
   cudaError_t e;
   if (launch_lanes<T, MODE>(a, st, e)) return e;
-  if (launch_cta<T, MODE>(a, st, e)) return e;
+  if constexpr (MODE != LM_PREFERENCE) {  // (that pass writes no gradient)
+    if (launch_cta<T, MODE>(a, st, e)) return e;
+  }
   if (launch_ring<T, MODE>(a, st, e)) return e;
-  return launch_wide<T, MODE>(a, st);
+  // the rings decline only rows that they would have to hold between two passes
+  if constexpr (MODE != LM_PREFERENCE && MODE != LM_SCALED) return launch_wide<T, MODE>(a, st);
+  return cudaErrorInvalidValue;
 }
 
 template <typename T>

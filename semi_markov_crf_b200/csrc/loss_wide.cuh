@@ -37,8 +37,7 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
   const Head h = make_head<MODE>(a, load_head<MODE>(a, r));
   const T* x = row_at<T>(a.x, r, a.ldx);
   T* g = a.g ? row_at<T>(a.g, r, a.ldg) : nullptr;
-  const float w = MODE == LM_SCALED && h.live ? a.wseq[h.b] : 0.0f;
-  bool blank = !h.live || h.malformed || (MODE == LM_SCALED && w == 0.0f);
+  bool blank = !h.live || h.malformed;
   bool malformed = h.live;
   const Range all{0, V, V};
   Teacher tc{dyn, reinterpret_cast<int*>(dyn + a.k), dyn + 2 * a.k, dyn + 3 * a.k,
@@ -59,45 +58,37 @@ __global__ void __launch_bounds__(WIDE_THREADS) loss_wide_kernel(const __grid_co
     malformed = tshare[1] == 1.0f;
   }
   if (blank) {
-    if (MODE != LM_SCALED && tid == 0) blank_outputs<MODE>(a, r, malformed);
+    if (tid == 0) blank_outputs<MODE>(a, r, malformed);
     if (g && !a.add)
       for (int v = tid; v < V; v += WIDE_THREADS) g[v] = from_f32<T>(0.0f);
     return;
   }
 
-  Base base;
-  float S, cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
-  if (MODE == LM_SCALED) {
-    base = unpack_stat(a.stat[r], S);
-    cy = (float)((double)w * a.s);
-    cq = -cy;
-  } else {
-    // maximum and sum of exponentials in one pass
-    float m = NEG_INF, s = 0.0f;
-    for (int v = tid; v < V; v += WIDE_THREADS) {
-      const float xv = to_f32<T>(x[v]);
-      if (xv > m) {
-        s *= ex2((m - xv) * a.sl);
-        m = xv;
-      }
-      s += ex2((xv - (m == NEG_INF ? 0.0f : m)) * a.sl);
+  // maximum and sum of exponentials in one pass
+  float m = NEG_INF, s = 0.0f;
+  for (int v = tid; v < V; v += WIDE_THREADS) {
+    const float xv = to_f32<T>(x[v]);
+    if (xv > m) {
+      s *= ex2((m - xv) * a.sl);
+      m = xv;
     }
-    const float M = wide_max(m, red);
-    S = wide_sum(m == NEG_INF && s == 0.0f ? 0.0f : s * ex2((m - M) * a.sl), red);
-    if (M == NEG_INF) S = quiet_nan();  // nothing but -inf: no distribution
-    base.at = M;
-    base.direct = false;
-    if (MODE == LM_DISTILL) {
-      P = tshare[0];
-      if (warp == 0) teacher_terms(a, r, tc, th, base, S, true, lane, 32, FULL_MASK);
-      cq = (float)((a.w ? a.w[h.b] : 1.0) * a.tau);
-      if (a.add) __syncthreads();  // the gradient's old values at the entries are read
-    } else {
-      cy = label_outputs<MODE>(a, r, load_label<T, MODE>(a, r, h, x), base, S, tid == 0);
-      cq = -cy;
-    }
+    s += ex2((xv - (m == NEG_INF ? 0.0f : m)) * a.sl);
   }
-  if (!g || MODE == LM_PREFERENCE) return;
+  const float M = wide_max(m, red);
+  float S = wide_sum(m == NEG_INF && s == 0.0f ? 0.0f : s * ex2((m - M) * a.sl), red);
+  if (M == NEG_INF) S = quiet_nan();  // nothing but -inf: no distribution
+  const Base base{M, false};
+  float cq, cy = 0.0f, P = 1.0f;  // gradient of the row: cq q_v, and cy more at the label
+  if (MODE == LM_DISTILL) {
+    P = tshare[0];
+    if (warp == 0) teacher_terms(a, r, tc, th, base, S, true, lane, 32, FULL_MASK);
+    cq = (float)((a.w ? a.w[h.b] : 1.0) * a.tau);
+    if (a.add) __syncthreads();  // the gradient's old values at the entries are read
+  } else {
+    cy = label_outputs<MODE>(a, r, load_label<T, MODE>(a, r, h, x), base, S, tid == 0);
+    cq = -cy;
+  }
+  if (!g) return;
   const float scale = __fdividef(cq * P, S);
   for (int v = tid; v < V; v += WIDE_THREADS) {
     float gv = based_exp(to_f32<T>(x[v]), a.sl, base) * scale;

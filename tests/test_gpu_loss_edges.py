@@ -447,3 +447,48 @@ def test_preferences_of_impossible_labels():
     y = torch.full((2, 1), 3, dtype=torch.int32, device="cuda")
     out = semicrf.preference_loss(x, n, y, beta=1.0, smoothing=1.0)
     assert out["loss"].tolist() == [0.0] and not bool(out["grad_logits"].any())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("pads", [(0, 0), (1, 1), (0, 3)], ids=str)
+def test_every_shape_of_short_rows(dtype, pads):
+    """Every number of lanes, elements and kept teacher's entries is compiled and
+    right: a row's log-probability within E + u |logp|, and its gradient, whose
+    entries sum to 0: each is rounded by half a step of its size and the softmax's
+    parts by E and 12 u, so that the sum is off by at most (half a step + E + 12 u)
+    times the sum of their sizes, 2 at most (float16: V halves of a subnormal step
+    more)."""
+    from semi_markov_crf_b200 import semicrf
+    n = torch.full((2,), 2, dtype=torch.int32, device="cuda")
+    y = torch.tensor([[0, 1], [2, 0]], dtype=torch.int32, device="cuda")
+    g = _gen(1)
+    noise = torch.randn(2, 2, 2060, generator=g, device="cuda")
+    teacher = torch.randn(2, 2, 300, generator=g, device="cuda")
+    for V in list(range(3, 280)) + list(range(280, 2049, 17)) + [511, 512, 513, 1023, 1024, 1025, 1032, 2047, 2048]:
+        x = torch.full((2, 2, V + pads[0]), math.nan, dtype=dtype, device="cuda")[..., :V]
+        x.copy_(noise[..., :V])
+        logq = torch.log_softmax(x.double(), -1)
+        logp = logq.gather(-1, y.long()[..., None])[..., 0]
+        E = sum_error(V)
+        near = lambda o: bool(((o["logp"] - logp).abs() <= E + U * logp.abs()).all())
+        buf = torch.empty(2, 2, V + pads[1], dtype=dtype, device="cuda")[..., :V]
+        tol = 2 * (HALF[dtype] + E + 12 * U) + V * TINY[dtype]
+        zero = lambda o: bool((o["grad_logits"].double().sum(-1).abs() <= tol).all())
+        assert near(semicrf.label_logprob(x, n, y)), V
+        pairs = semicrf.preference_loss(x, n, y, grad=False)
+        assert near(pairs), V
+        for call in (lambda o: semicrf.label_logprob(x, n, y, grad=True, out=o),
+                     lambda o: semicrf.policy_loss(x, n, y, logp.float(), noise[:, 0, 0].clamp(-1, 1), out=o),
+                     lambda o: semicrf.preference_loss(x, n, y, beta=1.0, out=o)):
+            out = call({"grad_logits": buf.fill_(math.nan)})
+            assert near(out) and zero(out), V
+        for k in (1, 3, 5, 9, 17, 33, 65, 128, 129, 300):
+            ids = (torch.arange(k, device="cuda", dtype=torch.int32) * 7 % V).expand(2, 2, k).contiguous()
+            t = teacher[..., :k].contiguous()
+            assert zero(semicrf.distill_loss(x, n, ids, t, out={"grad_logits": buf.fill_(math.nan)})), (V, k)
+            bare = semicrf.distill_loss(x, n, ids, t, grad=False)["token_loss"].double()
+            p = torch.softmax(t.double(), -1)
+            gap = p.log() - logq.gather(-1, ids.long())
+            want = (p * gap).sum(-1)
+            e = E + ((28 + k / 32 + 12) * U * (1 + gap.abs()) * p * (1 + gap.abs())).sum(-1)
+            assert bool(((bare - want).abs() <= e + 40 * U + U * want.abs()).all()), (V, k)
