@@ -208,6 +208,13 @@ __device__ __forceinline__ PolicyTerm<F> policy_term(F delta, F adv, F lo, F hi,
 // rows of 1000 bfloat16, loss and gradient, 214 against 206 us.)
 constexpr double POLICY_F32 = 64.0;
 
+// (apart, for its registers: inlined it made some 60 row kernels spill)
+static __device__ __noinline__ PolicyTerm<double> policy_term_far(double delta, double adv, double lo,
+                                                                  double hi, double c, bool has_ref,
+                                                                  double d) {
+  return policy_term<double>(delta, adv, lo, hi, c, has_ref, d);
+}
+
 __device__ __forceinline__ PolicyTerm<double> policy_term_of(double delta, double adv, double lo,
                                                              double hi, double c, bool has_ref,
                                                              double d) {
@@ -216,7 +223,7 @@ __device__ __forceinline__ PolicyTerm<double> policy_term_of(double delta, doubl
                                                    (float)c, has_ref, (float)d);
     return PolicyTerm<double>{o.loss, o.kl, o.slope, o.clipped};
   }
-  return policy_term<double>(delta, adv, lo, hi, c, has_ref, d);
+  return policy_term_far(delta, adv, lo, hi, c, has_ref, d);
 }
 
 }  // namespace semicrf
