@@ -492,3 +492,60 @@ def test_every_shape_of_short_rows(dtype, pads):
             want = (p * gap).sum(-1)
             e = E + ((28 + k / 32 + 12) * U * (1 + gap.abs()) * p * (1 + gap.abs())).sum(-1)
             assert bool(((bare - want).abs() <= e + 40 * U + U * want.abs()).all()), (V, k)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("op", OPS)
+def test_every_gradient_entry(op, dtype):
+    """Each entry of the gradient, written over NaN, at a width of every kernel:
+    the relative error of its softmax, not only that of its row's weight."""
+    for V, pad in ((39, 0), (150, 1), (1000, 0), (1999, 1), (2048, 8), (3001, 3), (8192, 0), (9001, 5),
+                   (20000, 0), (33001, 0), (131072, 0), (140000, 3), (300001, 0), (600001, 0),
+                   (900001, 1)):
+        p = Problem(_scores(4, 3, V, dtype, V, pad), [3, 0, 1, 3], tau=1.25, seed=V, k=40,
+                    lse=V % 2 == 1, average=V % 3 == 0)
+        p.check(op, p.call(op, pad=pad))
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("V", [150, 3001, 40000, 140001, 600001])
+def test_gradient_rows_on_other_boundaries(V, op):
+    """Scores and gradient rows that lie differently in their 16-byte vectors."""
+    for dtype in (torch.float32, torch.bfloat16):
+        p = Problem(_scores(2, 3, V, dtype, V, 3), [3, 2], seed=V)
+        p.check(op, p.call(op, pad=2))
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("V", [39, 1500, 5000, 8200, 40000, 140001, 600001])
+def test_accumulated_entries(V, op):
+    p = Problem(_scores(4, 3, V, torch.float32, V), [3, 0, 2, 3], tau=0.8, seed=V)
+    p.check(op, p.call(op, accumulate=True), accumulated=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("op", OPS)
+def test_losses_without_a_gradient(op, dtype):
+    for B, T in ((4, 3), (4, 1), (2, 300)):
+        for V, pad in ((6, 0), (39, 1), (128, 0), (777, 0), (2048, 0), (2049, 0), (5000, 3), (12000, 0),
+                       (40000, 1), (131072, 0), (300001, 0), (600001, 0)):
+            if T == 300 and V > 12000:
+                continue
+            lens = [T, T // 2, T, T - 1][:B]
+            p = Problem(_scores(B, T, V, dtype, V, pad), lens, tau=1.25, seed=V, k=30, lse=V % 2 == 1)
+            out = p.call(op, grad=False)
+            assert "grad_logits" not in out
+            p.check(op, out)
+
+
+@pytest.mark.parametrize("tau", [1e-3, 0.02, 50.0, 1e3])
+@pytest.mark.parametrize("op", OPS)
+def test_temperatures_to_their_limits(op, tau):
+    """Scores whose differences matter at the temperature, and scores of
+    ordinary size."""
+    for V in (39, 1500, 5000, 40000, 140001, 600001):
+        for dtype in (torch.float32, torch.bfloat16):
+            for scale in (2.5, 2.5 * tau):
+                p = Problem(_scores(2, 3, V, dtype, V, scale=scale), [3, 2], tau=tau, seed=V)
+                p.check(op, p.call(op))
+                p.check(op, p.call(op, grad=False))
