@@ -175,7 +175,8 @@ __device__ __forceinline__ F exp_less_linear(F d) {
     p = p * d + F(0.5);
     return p * d * d;
   }
-  return exp_of(d) - d - F(1);
+  const F e = exp_of(d);
+  return e > F(1e30) ? e : e - d - F(1);  // d may be infinite: a label of probability zero
 }
 
 // The clip is given by its corners lo = 1 - clip_low and hi = 1 + clip_high.

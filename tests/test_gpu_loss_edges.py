@@ -494,6 +494,35 @@ def test_every_shape_of_short_rows(dtype, pads):
             assert bool(((bare - want).abs() <= e + 40 * U + U * want.abs()).all()), (V, k)
 
 
+@pytest.mark.parametrize("V", [39, 5000, 40000])
+def test_divergence_from_an_impossible_label(V):
+    """A label of probability zero that the reference allows: the KL term is
+    infinite, and without its weight the loss and the gradient are finite; one that
+    only the reference excludes has an infinite term too."""
+    from semi_markov_crf_b200 import semicrf
+    x = _scores(3, 1, V, torch.float32, V)
+    x[0, 0, 2] = -math.inf
+    n = torch.ones(3, dtype=torch.int32, device="cuda")
+    y = torch.full((3, 1), 2, dtype=torch.int32, device="cuda")
+    old = torch.full((3, 1), -3.0, device="cuda")
+    ref = torch.tensor([[-2.0], [-math.inf], [-3.0]], device="cuda")
+    adv = torch.ones(3, device="cuda")
+    for c in (0.0, 0.1):
+        out = semicrf.policy_loss(x, n, y, old, adv, ref_logp=ref, kl_coef=c)
+        assert out["kl"][:2].tolist() == [math.inf] * 2 and math.isfinite(out["kl"][2])
+        assert out["logp"][0, 0].item() == -math.inf
+        assert [math.isfinite(v) for v in out["loss"].tolist()] == [c == 0.0, c == 0.0, True]
+        assert not torch.isnan(out["loss"]).any()
+        if c == 0.0:
+            assert torch.isfinite(out["grad_logits"]).all()
+            assert not bool(out["grad_logits"][0].any())
+    t = lambda *v: torch.tensor(v, dtype=torch.float64).cuda()
+    inf = math.inf
+    out = semicrf.policy_scores(t(-inf, -5.0, -2000.0), t(-3.0, -5.0, -2000.0), t(1.0, 1.0, 1.0),
+                                t(-2.0, -inf, 0.0), kl_coef=0.5)
+    assert out["kl"].tolist() == [inf, inf, inf] and out["loss"].tolist() == [inf, inf, inf]
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=str)
 @pytest.mark.parametrize("op", OPS)
 def test_every_gradient_entry(op, dtype):
