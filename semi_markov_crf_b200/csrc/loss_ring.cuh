@@ -81,9 +81,9 @@ constexpr int NOTE_DIRECT = 0, NOTE_DIFFERENCE = 1, NOTE_ZERO = 2;
 // What a teacher warp tells the scalar warp about a row.
 struct TeacherNote {
   float P;    // the entries' total probability
-  int blank;  // the row has no gradient: an entry's label is outside the range, or no
-              // entry has a probability
+  int blank;  // why the row has no gradient: ENTRY_OUTSIDE the labels, ENTRY_NONE in use
 };
+constexpr int ENTRY_OUTSIDE = 1, ENTRY_NONE = 2;
 
 // float32 words of a teacher warp's entries.
 __host__ __device__ inline size_t teacher_entry(int k, int V) {
@@ -400,20 +400,18 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
     // gradient rows of another alignment are stored element by element
     const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(g)) & 15) == 0;
     T* gb = g + p.sp.head + (size_t)p.lo * VE;
-    auto clear = [&](int from, int n) {  // zeros over n vectors, unless added to
-      if (a.add) return;
-      for (int v = from + gt; v < from + n; v += GT) {
-        if (same) {
-          reinterpret_cast<uint4*>(gb)[v] = make_uint4(0, 0, 0, 0);
-        } else {
-          for (int e = 0; e < VE; ++e) gb[(size_t)v * VE + e] = from_f32<T>(0.0f);
-        }
-      }
-    };
     wait(&st.note_full[turn.i], turn.phase);
     const RowNote note = st.note[turn.i];
-    if (note.kind == NOTE_ZERO && note.y < 0) {  // not read
-      clear(0, p.n);
+    if (note.kind == NOTE_ZERO && note.y < 0) {  // not read: zeros, unless added to
+      if (!a.add) {
+        for (int i = gt; i < p.n; i += GT) {
+          if (same) {
+            reinterpret_cast<uint4*>(gb)[i] = make_uint4(0, 0, 0, 0);
+          } else {
+            for (int e = 0; e < VE; ++e) gb[(size_t)i * VE + e] = from_f32<T>(0.0f);
+          }
+        }
+      }
     } else {
       const f32x2 at2 = pair(-note.at, -note.at), scale2 = pair(note.scale, note.scale);
       const bool plain = note.kind == NOTE_DIRECT && same && !a.add;
@@ -422,10 +420,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
         const uint4* chunk =
             reinterpret_cast<const uint4*>(pl.ring + (size_t)cur.slot * pl.chunk_bytes);
         const int have = p.n - c;
-        if (MODE == LM_DISTILL && note.kind == NOTE_ZERO) {  // read, but its teacher's entries leave nothing
-          give_back(wait, &st.empty[cur.slot], lane);
-          clear(c, min(have, chunk_vecs));
-        } else if (plain) {
+        if (plain) {
           uint4 raw[RING_NV];
           take_chunk<T>(raw, chunk, gt, GT, have);
 #pragma unroll
@@ -456,8 +451,9 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
             T* to = gb + (size_t)(c + at) * VE;
 #pragma unroll 1
             for (int e = 0; e < VE; ++e) {
-              const Base base{note.at, note.kind == NOTE_DIRECT};
-              float gv = based_exp(to_f32<T>(each[e]), a.sl, base) * note.scale;
+              float gv = 0.0f;
+              if (note.kind == NOTE_DIRECT) gv = ex2(fmaf(to_f32<T>(each[e]), a.sl, -note.at)) * note.scale;
+              if (note.kind == NOTE_DIFFERENCE) gv = ex2((to_f32<T>(each[e]) - note.at) * a.sl) * note.scale;
               if (a.add) gv += to_f32<T>(to[e]);
               to[e] = from_f32<T>(gv);
             }
@@ -593,7 +589,10 @@ __device__ __forceinline__ bool ring_scalar(const RowArgs& a, const RingPlace& p
       } else if (MODE == LM_DISTILL) {
         wait(&st.teacher_full[teacher.slot], teacher.phase);
         P = st.teacher[teacher.slot].P;
-        zero = st.teacher[teacher.slot].blank;
+        // without an entry P is 0, and so is the row's factor: its writers need not be
+        // told, unless the row has no sum
+        const int blank_entries = st.teacher[teacher.slot].blank;
+        zero = blank_entries == ENTRY_OUTSIDE || (blank_entries == ENTRY_NONE && !(S <= F32_MAX));
         cq = (float)(in.w * a.tau);
       } else {
         cy = label_outputs<MODE>(a, r, in, base, S, lane == 0 && pl.rank == 0);
@@ -672,7 +671,7 @@ __device__ __forceinline__ void ring_teacher(const RowArgs& a, const RingPlace& 
     }
     __syncwarp();  // (accumulation: all have read the values that the writers will change)
     if (lane == 0) {
-      st.teacher[me] = TeacherNote{th.P, th.malformed || th.none};
+      st.teacher[me] = TeacherNote{th.P, th.malformed ? ENTRY_OUTSIDE : th.none ? ENTRY_NONE : 0};
       wait.arrive(&st.teacher_full[me]);
     }
     own ^= 1;
