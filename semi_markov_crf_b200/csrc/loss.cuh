@@ -17,6 +17,16 @@ constexpr int LOSS_K_MAX = 1024;               // teacher entries per position
 // LM_SCALED: the gradient pass of the preference loss, g = wseq_b / temperature ([v = y] - q_v)
 // from the statistics that its first pass left.
 enum LossMode : int { LM_LOGPROB = 0, LM_POLICY = 1, LM_PREFERENCE = 2, LM_DISTILL = 3, LM_SCALED = 4 };
+// Sites of the bounds-checking build, after the recursions' (ring.cuh).
+enum LossSite : int {
+  SITE_LOSS_SCORE = 14,   // a row's element at a label or a teacher's entry
+  SITE_LOSS_EDGE = 15,    // a single element beside a row's 16-byte vectors
+  SITE_LOSS_VECTOR = 16,  // a vector of a row, read or written
+  SITE_LOSS_ENTRY = 17,   // a teacher's entry in shared memory, its word of the table
+  SITE_LOSS_CHUNK = 18,   // a chunk's source inside its row, its place inside the ring
+  SITE_LOSS_SLOT = 19,    // a slot of a ring's state, of this CTA or of a peer
+  SITE_LOSS_SUM = 20      // a position of a sequence, a CTA's place among the sums
+};
 enum LossType : int { LT_F32 = 0, LT_BF16 = 1, LT_F16 = 2 };
 
 // Everything a row kernel reads or writes.  Row r = b * T + t; z = x / temperature.

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(L, 640 / L)
   const T* x = row_at<T>(a.x, r, a.ldx);
   T* g = a.g ? row_at<T>(a.g, r, a.ldg) : nullptr;
   const Split sp = split_row(x, V);
-  const int ei = tid < sp.edge ? edge_index<T>(sp, tid) : -1;
+  const int ei = tid < sp.edge && edge_inside(a, edge_index<T>(sp, tid)) ? edge_index<T>(sp, tid) : -1;
   auto fill_zero = [&]() {
     if (!g || a.add) return;
     uint4* out = reinterpret_cast<uint4*>(g + sp.head);
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(L, 640 / L)
   for (int i = 0; i < NV; ++i) {
     constexpr uint32_t none = Vec<T>::LOWEST;
     q[i] = make_uint4(none, none, none, none);
-    if (i * L + tid < sp.nb) q[i] = __ldg(reinterpret_cast<const uint4*>(x + sp.head) + (i * L + tid));
+    if (i * L + tid < sp.nb && vector_inside<T>(a, sp, i * L + tid)) q[i] = __ldg(reinterpret_cast<const uint4*>(x + sp.head) + (i * L + tid));
   }
   float xe = NEG_INF;
   if (ei >= 0) xe = to_f32<T>(x[ei]);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(L, 640 / L)
   uint4* out = reinterpret_cast<uint4*>(g + sp.head);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if (i * L + tid >= sp.nb) continue;
+    if (i * L + tid >= sp.nb || !vector_inside<T>(a, sp, i * L + tid)) continue;
     f32x2 two[VE / 2];
 #pragma unroll
     for (int e = 0; e < VE / 2; ++e) two[e] = mul2(v[i * (VE / 2) + e], scale2);

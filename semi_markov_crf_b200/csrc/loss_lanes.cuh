@@ -67,12 +67,12 @@ __device__ __forceinline__ void lane_load(const RowArgs& a, LaneLoad<T, NE, LAY,
     for (int i = 0; i < NE / VE; ++i) {
       constexpr uint32_t none = Vec<T>::LOWEST;
       l.x.q[i] = make_uint4(none, none, none, none);
-      if (i * L + lane < sp.nb)
+      if (i * L + lane < sp.nb && vector_inside<T>(a, sp, i * L + lane))
         l.x.q[i] = __ldg(reinterpret_cast<const uint4*>(x + sp.head) + (i * L + lane));
     }
     if (LAY == SPLIT) {
       l.x.e[0] = from_f32<T>(NEG_INF);
-      if (lane < sp.edge) l.x.e[0] = x[edge_index<T>(sp, lane)];
+      if (lane < sp.edge && edge_inside(a, edge_index<T>(sp, lane))) l.x.e[0] = x[edge_index<T>(sp, lane)];
     }
   } else {
 #pragma unroll
@@ -112,7 +112,8 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
         const int id = now.ahead.id[u];
         if (id >= V) out = 1.0f;
         if (id < 0 || id >= V) now.ahead.t[u] = NEG_INF;
-        tx[u] = id >= 0 && id < V ? to_f32<T>(x[id]) : 0.0f;
+        tx[u] = 0.0f;
+        if (id >= 0 && id < V && SEMICRF_INB(a.status, id < a.V, SITE_LOSS_SCORE)) tx[u] = to_f32<T>(x[id]);
         m = fmaxf(m, now.ahead.t[u]);
       }
       th.malformed = lanes_max(out, L, mm) > 0.0f;
@@ -222,7 +223,7 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
     uint4* out = reinterpret_cast<uint4*>(g + sp.head);
 #pragma unroll
     for (int i = 0; i < NE / VE; ++i) {
-      if (i * L + lane >= sp.nb) continue;
+      if (i * L + lane >= sp.nb || !vector_inside<T>(a, sp, i * L + lane)) continue;
       f32x2 two[VE / 2];
 #pragma unroll
       for (int e = 0; e < VE / 2; ++e) two[e] = v[i * (VE / 2) + e];
@@ -236,7 +237,7 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
     }
     if (LAY == SPLIT && lane < sp.edge) {
       const int at = edge_index<T>(sp, lane);
-      g[at] = from_f32<T>(xe * scale + (a.add ? to_f32<T>(g[at]) : 0.0f));
+      if (edge_inside(a, at)) g[at] = from_f32<T>(xe * scale + (a.add ? to_f32<T>(g[at]) : 0.0f));
     }
   } else {
 #pragma unroll
@@ -276,7 +277,7 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
       float twice = 0.0f;
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u)
-        if (now.ahead.id[u] >= 0 && teacher_again(tc.table, size, V, now.ahead.id[u])) twice = 1.0f;
+        if (now.ahead.id[u] >= 0 && teacher_again(a, tc.table, size, V, now.ahead.id[u])) twice = 1.0f;
       repeats = lanes_max(twice, L, mm) > 0.0f;
       if (!repeats)
 #pragma unroll
@@ -303,7 +304,7 @@ __device__ __forceinline__ void lane_row(const RowArgs& a, LaneLoad<T, NE, LAY, 
     }
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
-      if (first[u]) {
+      if (first[u] && SEMICRF_INB(a.status, now.ahead.id[u] >= 0 && now.ahead.id[u] < V, SITE_LOSS_SCORE)) {
         const int id = now.ahead.id[u];
         // where the call accumulates, the row's own term is in already
         const float own = a.add ? to_f32<T>(g[id]) : based_exp(tx[u], a.sl, base) * scale;

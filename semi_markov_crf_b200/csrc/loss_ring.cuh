@@ -275,7 +275,7 @@ __device__ __forceinline__ void ring_copier(const RowArgs& a, unsigned char* rin
   HeadStream<MODE> heads{};
   if (!done) heads.load(a, r, pl.rows);
   Cursor cur{0, 0};
-  const unsigned char* src = nullptr;
+  const unsigned char *src = nullptr, *row = nullptr;
   int left = 0, idle = 0;
   while (!__all_sync(FULL_MASK, done)) {
     bool moved = false;
@@ -289,7 +289,8 @@ __device__ __forceinline__ void ring_copier(const RowArgs& a, unsigned char* rin
         if (!blank) {
           const T* x = row_at<T>(a.x, pass_row<MODE>(r, pl.rows), a.ldx);
           const Part p = part_of(x, a.V, pl.rank, pl.cl);
-          src = reinterpret_cast<const unsigned char*>(x + p.sp.head) + (size_t)p.lo * 16;
+          row = reinterpret_cast<const unsigned char*>(x);
+          src = row + (size_t)p.sp.head * sizeof(T) + (size_t)p.lo * 16;
           left = p.n * 16;
           open = left > 0;
         }
@@ -299,12 +300,20 @@ __device__ __forceinline__ void ring_copier(const RowArgs& a, unsigned char* rin
       moved = true;
     } else if (open && mbar_test(&st.empty[cur.slot], cur.phase ^ 1)) {
       const int n = min(left, pl.chunk_bytes);
-      mbar_expect_tx(&st.full[cur.slot], n);
-      bulk_g2s(ring + (size_t)cur.slot * pl.chunk_bytes, src, n, &st.full[cur.slot]);
-      src += n;
-      left -= n;
-      open = left > 0;
-      cur.next(pl.slots);
+      if (SEMICRF_INB(a.status, cur.slot >= 0 && cur.slot < pl.slots && n > 0 && n % 16 == 0 &&
+                                    reinterpret_cast<uintptr_t>(src) % 16 == 0 && src >= row &&
+                                    src + n <= row + (size_t)a.V * sizeof(T),
+                      SITE_LOSS_CHUNK)) {
+        mbar_expect_tx(&st.full[cur.slot], n);
+        bulk_g2s(ring + (size_t)cur.slot * pl.chunk_bytes, src, n, &st.full[cur.slot]);
+        src += n;
+        left -= n;
+        open = left > 0;
+        cur.next(pl.slots);
+      } else {
+        open = false;  // whoever waits for the chunk gives up
+        done = true;
+      }
       moved = true;
     }
     if (__any_sync(FULL_MASK, moved)) {
@@ -373,7 +382,7 @@ __device__ __forceinline__ void ring_reduce(const RowArgs& a, const RingPlace& p
     }
     join_lanes(mb, s);
     wait(&st.red_free[turn.i], turn.phase ^ 1);
-    if (lane == 0) {
+    if (lane == 0 && SEMICRF_INB(a.status, gw >= 0 && gw < RING_WARPS, SITE_LOSS_SLOT)) {
       st.red[turn.i][gw] = make_float2(mb, s);
       wait.arrive(&st.red_full[turn.i]);
     }
@@ -405,6 +414,7 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
     if (note.kind == NOTE_ZERO && note.y < 0) {  // not read: zeros, unless added to
       if (!a.add) {
         for (int i = gt; i < p.n; i += GT) {
+          if (!vector_inside<T>(a, p.sp, p.lo + i)) continue;
           if (same) {
             reinterpret_cast<uint4*>(gb)[i] = make_uint4(0, 0, 0, 0);
           } else {
@@ -436,17 +446,18 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
           uint4* out = reinterpret_cast<uint4*>(gb) + c + gt;
           if (have >= chunk_vecs) {
 #pragma unroll
-            for (int i = 0; i < RING_NV; ++i) out[i * GT] = raw[i];
+            for (int i = 0; i < RING_NV; ++i)
+              if (vector_inside<T>(a, p.sp, p.lo + c + gt + i * GT)) out[i * GT] = raw[i];
           } else {
 #pragma unroll
             for (int i = 0; i < RING_NV; ++i)
-              if (i * GT + gt < have) out[i * GT] = raw[i];
+              if (i * GT + gt < have && vector_inside<T>(a, p.sp, p.lo + c + gt + i * GT)) out[i * GT] = raw[i];
           }
         } else {
 #pragma unroll 1
           for (int i = 0; i < RING_NV; ++i) {
             const int at = i * GT + gt;
-            if (at >= have) break;
+            if (at >= have || !vector_inside<T>(a, p.sp, p.lo + c + at)) break;
             const T* each = reinterpret_cast<const T*>(chunk + at);
             T* to = gb + (size_t)(c + at) * VE;
 #pragma unroll 1
@@ -465,7 +476,8 @@ __device__ __forceinline__ void ring_write(const RowArgs& a, const RingPlace& pl
       if (has_label(MODE)) {
         // the thread that wrote the label's element puts it right
         const int at = note.y - p.sp.head - p.lo * VE;
-        if (at >= 0 && at < p.n * VE && at / VE % GT == gt)
+        if (at >= 0 && at < p.n * VE && at / VE % GT == gt &&
+            SEMICRF_INB(a.status, note.y < a.V, SITE_LOSS_SCORE))
           g[note.y] = from_f32<T>(a.add ? to_f32<T>(g[note.y]) + note.cy : note.gy);
       }
     }
@@ -511,7 +523,8 @@ __device__ __forceinline__ bool ring_scalar(const RowArgs& a, const RingPlace& p
     const T* x = row_at<T>(a.x, r, a.ldx);
     T* g = GRAD ? row_at<T>(a.g, r, a.ldg) : nullptr;
     const Part p = part_of(x, a.V, pl.rank, pl.cl);
-    const int ei = pl.rank == 0 && lane < p.sp.edge ? edge_index<T>(p.sp, lane) : -1;
+    int ei = pl.rank == 0 && lane < p.sp.edge ? edge_index<T>(p.sp, lane) : -1;
+    if (ei >= 0 && !edge_inside(a, ei)) ei = -1;
     RowNote note{};
     note.kind = NOTE_ZERO;
     note.y = -1;
@@ -548,7 +561,8 @@ __device__ __forceinline__ bool ring_scalar(const RowArgs& a, const RingPlace& p
           uint64_t* bar = &st.peer[rows_read.i];
           if (lane == 0 && !wait.dead) mbar_expect_tx(bar, 8 * pl.cl);
           __syncwarp();
-          if (lane < pl.cl && !wait.dead) {
+          if (lane < pl.cl && !wait.dead &&
+              SEMICRF_INB(a.status, pl.cl <= RING_CLUSTER_MAX && pl.rank < pl.cl, SITE_LOSS_SLOT)) {
             st_async_cluster(&st.part[rows_read.i][pl.rank].x, bar, lane, mb);
             st_async_cluster(&st.part[rows_read.i][pl.rank].y, bar, lane, s);
           }

@@ -168,7 +168,7 @@ __device__ __forceinline__ LabelIn<T> load_label(const RowArgs& a, long long r, 
   if (MODE == LM_DISTILL && a.tlse) in.lse = a.tlse[r];
   if (MODE == LM_SCALED) in.stat = a.stat[r];
   if (!has_label(MODE)) return in;
-  in.score = x[h.y];
+  if (SEMICRF_INB(a.status, h.y >= 0 && h.y < a.V, SITE_LOSS_SCORE)) in.score = x[h.y];
   if (MODE == LM_LOGPROB) in.slope = a.grad_logp ? a.grad_logp[r] : 1.0f;
   if (MODE == LM_PREFERENCE || MODE == LM_POLICY) in.ref_logp = a.ref_logp ? a.ref_logp[r] : 0.0f;
   if (MODE == LM_POLICY) {
@@ -283,11 +283,13 @@ __device__ __forceinline__ void teacher_clear(int* table, int size, int V, int l
 
 // Whether the label was there; it is from now on.  (A hash table is at least half
 // empty, so that every probe ends.)
-__device__ __forceinline__ bool teacher_again(int* table, int size, int V, int id) {
+__device__ __forceinline__ bool teacher_again(const RowArgs& a, int* table, int size, int V, int id) {
   if (size == teacher_bits(V)) {
+    if (!SEMICRF_INB(a.status, id >= 0 && id >> 5 < size, SITE_LOSS_ENTRY)) return false;
     const unsigned bit = 1u << (id & 31);
     return atomicOr(reinterpret_cast<unsigned*>(&table[id >> 5]), bit) & bit;
   }
+  if (!SEMICRF_INB(a.status, size >= 2 && (size & (size - 1)) == 0, SITE_LOSS_ENTRY)) return false;
   for (unsigned at = teacher_slot(id, size);; ++at) {
     const int was = atomicCAS(&table[at & (size - 1)], -1, id);
     if (was == -1 || was == id) return was == id;
@@ -395,7 +397,7 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
     for (int u = 0; u < TEACHER_AHEAD; ++u) {
       const bool inside = ahead.id[u] >= 0 && ahead.id[u] < a.V;
       xs[u] = from_f32<T>(0.0f);
-      if (inside) xs[u] = x[ahead.id[u]];
+      if (inside && SEMICRF_INB(a.status, ahead.id[u] < a.V, SITE_LOSS_SCORE)) xs[u] = x[ahead.id[u]];
       if (ahead.id[u] >= a.V) out = 1.0f;
       if (!inside) ahead.id[u] = -1;
     }
@@ -427,7 +429,7 @@ __device__ __forceinline__ TeacherHead teacher_head(const RowArgs& a, long long 
     __syncwarp(mm);
     float twice = 0.0f;
     for (int j = lane; j < a.k; j += n)
-      if (tc.id[j] >= 0 && teacher_again(tc.table, size, a.V, tc.id[j])) twice = 1.0f;
+      if (tc.id[j] >= 0 && teacher_again(a, tc.table, size, a.V, tc.id[j])) twice = 1.0f;
     th.repeats = lanes_max(twice, n, mm) > 0.0f;
   }
   return th;
@@ -459,7 +461,7 @@ __device__ __forceinline__ void teacher_fix(const RowArgs& a, const Teacher& tc,
 #pragma unroll 4
   for (int j = lane; j < a.k; j += n) {
     const int id = tc.id[j];
-    if (id < 0 || !rg.has(id)) continue;
+    if (id < 0 || !rg.has(id) || !SEMICRF_INB(a.status, id < a.V, SITE_LOSS_SCORE)) continue;
     float p = tc.p[j];
     if (repeats) {
       bool first = true;
@@ -636,6 +638,15 @@ __device__ __forceinline__ Split split_row(const T* x, int V) {
 template <typename T>
 __device__ __forceinline__ int edge_index(const Split& s, int i) {
   return i < s.head ? i : s.nb * vec_of<T> + i;
+}
+
+// Whether vector i of a row (from its first 16-byte boundary) lies inside it.
+template <typename T>
+__device__ __forceinline__ bool vector_inside(const RowArgs& a, const Split& s, int i) {
+  return SEMICRF_INB(a.status, i >= 0 && i < s.nb && s.head + (i + 1) * vec_of<T> <= a.V, SITE_LOSS_VECTOR);
+}
+__device__ __forceinline__ bool edge_inside(const RowArgs& a, int at) {
+  return SEMICRF_INB(a.status, at >= 0 && at < a.V, SITE_LOSS_EDGE);
 }
 
 #include "loss_lanes.cuh"

@@ -48,8 +48,8 @@ struct SumState {
 // the cluster, in a fixed order; complete in every thread of CTA 0.  `value`:
 // (array, position) -> double.  Every thread of every CTA calls it.
 template <int N, typename F>
-__device__ __forceinline__ void sequence_sums(int n, int rank, int ctas, SumState& st, F value,
-                                              double (&out)[N]) {
+__device__ __forceinline__ void sequence_sums(int n, int T, int* status, int rank, int ctas, SumState& st,
+                                              F value, double (&out)[N]) {
   const int threads = blockDim.x, tid = threadIdx.x;
   double s[N] = {};
   for (long long t0 = (long long)rank * threads * SUM_UNROLL + tid; t0 < n;
@@ -60,7 +60,7 @@ __device__ __forceinline__ void sequence_sums(int n, int rank, int ctas, SumStat
 #pragma unroll
       for (int u = 0; u < SUM_UNROLL; ++u) {
         const long long t = t0 + (long long)u * threads;
-        v[u] = t < n ? value(k, (int)t) : 0.0;
+        v[u] = t < n && SEMICRF_INB(status, t >= 0 && t < T, SITE_LOSS_SUM) ? value(k, (int)t) : 0.0;
       }
 #pragma unroll
       for (int u = 0; u < SUM_UNROLL; ++u) s[k] += v[u];
@@ -74,7 +74,7 @@ __device__ __forceinline__ void sequence_sums(int n, int rank, int ctas, SumStat
     if ((tid & 31) == 0) st.warp[k][tid >> 5] = v;
   }
   __syncthreads();
-  if (tid < N) {
+  if (tid < N && SEMICRF_INB(status, rank >= 0 && rank < ctas && ctas <= SUM_CTAS, SITE_LOSS_SUM)) {
     double v = 0.0;
     for (int i = 0; i < threads / 32; ++i) v += st.warp[tid][i];
     // to CTA 0 of the cluster
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(SUM_THREADS) loss_sums_kernel(SeqArgs a, int c
   const bool bad = L < 0 || L > a.T;
   const long long row = (long long)b * a.T;
   double out[3];
-  sequence_sums<3>(bad ? 0 : L, rank, ctas, st, [&](int k, int t) -> double {
+  sequence_sums<3>(bad ? 0 : L, a.T, a.status, rank, ctas, st, [&](int k, int t) -> double {
     if (k == 0) return a.sum ? (double)a.tok[row + t] : 0.0;
     if (k == 1) return a.kl_sum ? (double)a.kl[row + t] : 0.0;
     return a.clipped ? (double)a.clip[row + t] : 0.0;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(SUM_THREADS) loss_pairs_kernel(SeqArgs a, int 
     off[side] = L < 0 || L > a.T;
     const long long row = (long long)b * a.T;
     double out[2];
-    sequence_sums<2>(off[side] ? 0 : L, rank, ctas, st, [&](int k, int t) -> double {
+    sequence_sums<2>(off[side] ? 0 : L, a.T, a.status, rank, ctas, st, [&](int k, int t) -> double {
       if (k == 0) return (double)a.tok[row + t];
       return a.average && a.labels[row + t] >= 0 ? 1.0 : 0.0;
     }, out);
