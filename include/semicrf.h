@@ -364,7 +364,10 @@ SEMICRF_API int semicrf_path_score_proj(const float *em, const int32_t *lengths,
  *    and its gradient row are NaN.  -inf beside finite scores is a label of
  *    probability zero.
  *  - Sums of exponentials are float32 around the row's maximum; log-probabilities,
- *    ratios and sums over positions are float64, each output rounded once.
+ *    log-ratios and sums over positions are float64.  float32, as the outputs, are
+ *    the exponentials of log-ratios up to 64 and the policy terms made of them
+ *    (float64 beyond), a teacher's probabilities and terms, every position's term
+ *    before it is summed, and the weight of a position's gradient row.
  *    Results are deterministic (no floating-point atomics).
  */
 enum semicrf_dtype { SEMICRF_F32 = 0, SEMICRF_BF16 = 1, SEMICRF_F16 = 2 };
