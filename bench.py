@@ -10,8 +10,10 @@ Metric: edge evaluations per second, edges = sum_b L_b * K * C^2 per step.
 The headline workload is the largest single-GPU configuration, the
 large-label batch (B=8, T=10,000, K=64, C=128: 8.4e10 edges per pass).  The
 same line carries one entry per other workload under "workloads" (speech,
-genomic, ultra, tiny), each timed the same way with its own roofline,
-itemised peak memory and a sampled CPU-oracle baseline.
+genomic, ultra, tiny), each timed the same way, with its roofline, peak memory
+and CPU-oracle baseline in brief, so that the line stays short enough for
+readers that keep only the last kilobytes of a program's output; the entries in
+full (per kernel, itemised memory) go to standard error, a JSON line each.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
                     [--workload NAME] [--extras a,b,...|none]
@@ -555,6 +557,23 @@ def measure(wl: Workload, steps: int, warmup: int, flush, world: int, local: int
     return res, graph
 
 
+def brief(entry):
+    """A further workload's entry as the one line carries it."""
+    keep = ("workload", "B", "T", "K", "C", "ms_per_step", "value", "positions_per_s",
+            "gpu_launches_per_step", "step_mufu_frac")
+    out = {k: entry[k] for k in keep if k in entry}
+    if "memory" in entry:
+        out["peak_hbm_bytes"] = entry["memory"]["peak_bytes"]
+    if entry.get("roofline"):
+        out["roofline"] = {k: entry["roofline"][k] for k in ("kernel", "bound", "frac")
+                           if k in entry["roofline"]}
+    if entry.get("clocks"):
+        out["clocks"] = {k: entry["clocks"][k] for k in ("sm_mhz", "reasons") if k in entry["clocks"]}
+    if "cpu_baseline" in entry:
+        out["cpu_baseline_value"] = entry["cpu_baseline"]["value"]
+    return out
+
+
 def run_ours(args):
     import torch
     import torch.distributed as dist
@@ -703,7 +722,9 @@ def run_ours(args):
         if world == 1 and not args.no_cpu_baseline:
             line["cpu_baseline"] = cpu_baseline(name, wl.w)
         if extras:
-            line["workloads"] = extras
+            line["workloads"] = {k: brief(v) for k, v in extras.items()}
+            for v in extras.values():
+                print(json.dumps(v), file=sys.stderr, flush=True)
         print(json.dumps(line), flush=True)
     if world > 1:
         dist.barrier()
