@@ -46,7 +46,7 @@ int check_sizes(int B, int T) {
 
 bool is_finite(double v) { return std::isfinite(v); }
 
-// An array of a call; a null one overlaps nothing.
+// An array of a call; a null or empty one overlaps nothing.
 struct Span {
   const void* p;
   size_t bytes;
@@ -58,7 +58,7 @@ bool overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> in
   for (const Span& o : outputs)
     for (const Span& i : inputs) {
       const uintptr_t po = (uintptr_t)o.p, pi = (uintptr_t)i.p;
-      if (po && pi && po < pi + i.bytes && pi < po + o.bytes) return true;
+      if (po && pi && o.bytes && i.bytes && po < pi + i.bytes && pi < po + o.bytes) return true;
     }
   return false;
 }
